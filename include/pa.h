@@ -364,6 +364,64 @@ PA_API pa_status pa_swap_blocks(const void *src_k, const void *src_v, int src_bl
                                 int head_dim, int block_size, pa_dtype dtype,
                                 cudaStream_t stream);
 
+/* ------------------------------------------------------------------------
+ * Decoding over part of a paged cache (page "字节跳动 AI Infra (2)",
+ * algorithm-level table, sparse attention row, and its KV table, H2O row:
+ * attend to, or keep, the important tokens only). Two ways:
+ *   - all tokens stay cached and each step reads a few blocks of them:
+ *     pa_update_key_bounds after the append, pa_select_blocks, then
+ *     pa_decode_selected_blocks;
+ *   - the cache itself is cut back: pa_decode_accumulate_weights in place of
+ *     pa_decode, and pa_evict_tokens when a sequence has outgrown its budget
+ *     (then pa_update_key_bounds over the kept tokens if bounds are in use).
+ * All take fp32 or bf16 caches; num_seqs and num_kv_heads at most 65535. */
+
+/* Elementwise minimum and maximum of each block's valid keys, refreshed for
+ * the blocks that hold the last new_lens[b] tokens of each row b:
+ *   key_bounds[p][h][0][d] = min, key_bounds[p][h][1][d] = max of K_j[d] over
+ *   the valid tokens j < context_lens[b] of physical block p, for the blocks
+ *   of positions [context_lens[b] - new_lens[b], context_lens[b]).
+ *   key_bounds   [num_blocks][num_kv_heads][2][head_dim], element type
+ *                `dtype`, 16-byte aligned, as many blocks as the cache. Bounds
+ *                of other blocks are left as they were. Values are exact; a
+ *                NaN key makes its dimension's bounds NaN.
+ *   new_lens     int32 [num_seqs]: 1 after a decode step's append, a chunk's
+ *                length after a prefill chunk's, 0 for a row to be left alone.
+ *   max_new_len  host-side upper bound of new_lens.
+ * A new_lens[b] outside [0, min(context_lens[b], max_new_len)], or a
+ * context_lens[b] outside [0, max_blocks_per_seq*block_size], is clamped and
+ * recorded as PA_ERR_BAD_TABLE. Rows that share a touched block must agree on
+ * its valid tokens (a block shared before its copy on write does). */
+PA_API pa_status pa_update_key_bounds(void *key_bounds, const void *k_cache,
+                                      const int32_t *block_tables, const int32_t *context_lens,
+                                      const int32_t *new_lens, int num_seqs, int max_new_len,
+                                      int num_kv_heads, int head_dim, int block_size,
+                                      int num_blocks, int max_blocks_per_seq, pa_dtype dtype,
+                                      cudaStream_t stream);
+
+/* The blocks worth attending to, for each row and K/V head. Block j of row b
+ * (j < n, n = ceil(context_lens[b] / block_size)) has the score
+ *   s_j = max over the query heads g of K/V head h of
+ *         sum_d max(q[b][g][d], 0) * hi_j[d] + min(q[b][g][d], 0) * lo_j[d]
+ * with lo, hi its key_bounds: an upper bound of q . K over the block's keys.
+ * selected[b][h] lists min(n, max_selected) block indices (places in row b's
+ * table, not physical ids) in ascending order, then -1: all n blocks when
+ * n <= max_selected, else the first num_first, the last num_last and those of
+ * largest score between them. Scores are compared in 64 bits; equal scores go
+ * to the lower index, and a NaN score ranks above every number.
+ *   selected     int32 [num_seqs][num_kv_heads][max_selected]
+ *   max_selected > 0; num_first + num_last <= max_selected.
+ *   max_context_len  host-side upper bound of context_lens, as in pa_decode;
+ *                at most 196608 blocks.
+ * A block id outside the pool ranks below every score and is recorded as
+ * PA_ERR_BAD_TABLE. */
+PA_API pa_status pa_select_blocks(int32_t *selected, const void *q, const void *key_bounds,
+                                  const int32_t *block_tables, const int32_t *context_lens,
+                                  int max_selected, int num_first, int num_last, int num_seqs,
+                                  int num_q_heads, int num_kv_heads, int head_dim,
+                                  int block_size, int num_blocks, int max_blocks_per_seq,
+                                  int max_context_len, pa_dtype dtype, cudaStream_t stream);
+
 /* Check block tables and lengths on the device: every entry a row's valid
  * tokens reach must lie in [0, num_blocks), and 0 <= context_lens[r] <=
  * max_blocks_per_seq*block_size. d_scratch is one caller-owned device int32.

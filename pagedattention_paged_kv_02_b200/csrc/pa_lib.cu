@@ -7,6 +7,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 #include <cstdlib>
@@ -23,6 +24,8 @@
 #include "decode_fp8.cuh"
 #include "prefill.cuh"
 #include "blocks.cuh"
+#include "key_bounds.cuh"
+#include "select_blocks.cuh"
 
 namespace {
 
@@ -1105,3 +1108,6 @@ extern "C" pa_status pa_decode_static_workspace(
                      max_context_len, scale, partition_size, ws, kStaticWorkspaceBytes, dtype,
                      stream);
 }
+
+// ------------------------------------- decoding over part of a paged cache
+#include "pa_sparse.cuh"

@@ -28,7 +28,8 @@ EXPORTS = ("pa_reshape_and_cache", "pa_decode_workspace_size", "pa_decode_partit
            "pa_decode_static_workspace", "pa_copy_blocks", "pa_swap_blocks",
            "pa_reshape_and_cache_fp8", "pa_decode_fp8", "pa_decode_sliding_window",
            "pa_prefill_chunk_sliding_window", "pa_reshape_and_cache_int8", "pa_decode_int8",
-           "pa_decode_shared_prefix", "pa_decode_shared_prefix_workspace_size")
+           "pa_decode_shared_prefix", "pa_decode_shared_prefix_workspace_size",
+           "pa_update_key_bounds", "pa_select_blocks")
 
 
 class PAError(RuntimeError):
@@ -71,6 +72,8 @@ def lib() -> ctypes.CDLL:
                                               I, I, I, F, I, P, SZ, I, P]
         L.pa_decode_shared_prefix_workspace_size.argtypes = [I, I, I, I, I, I, I, I, I]
         L.pa_decode_shared_prefix_workspace_size.restype = SZ
+        L.pa_update_key_bounds.argtypes = [P, P, P, P, P, I, I, I, I, I, I, I, I, P]
+        L.pa_select_blocks.argtypes = [P, P, P, P, P, I, I, I, I, I, I, I, I, I, I, I, I, P]
         L.pa_copy_blocks.argtypes = [P, P, P, I, I, I, I, I, I, P]
         L.pa_swap_blocks.argtypes = [P, P, I, P, P, I, P, I, I, I, I, I, P]
         L.pa_check_tables.argtypes = [P, P, I, I, I, I, P, ctypes.POINTER(I), P]
@@ -83,7 +86,8 @@ def lib() -> ctypes.CDLL:
                   "pa_reshape_and_cache_fp8", "pa_decode_fp8", "pa_decode_sliding_window",
                   "pa_prefill_chunk_sliding_window", "pa_reshape_and_cache_int8",
                   "pa_decode_int8", "pa_decode_shared_prefix", "pa_device_error",
-                  "pa_selftest_bounded_wait", "pa_decode_partition_tokens", "pa_version"):
+                  "pa_selftest_bounded_wait", "pa_decode_partition_tokens", "pa_version",
+                  "pa_update_key_bounds", "pa_select_blocks"):
             getattr(L, f).restype = I
         _lib = L
     return _lib
@@ -529,3 +533,106 @@ def prepare_decode_fp8(out, q, k_cache, v_cache, k_scale, v_scale, block_tables,
                      block_tables.shape[1], int(max_context_len), float(scale),
                      int(partition_size), _p(workspace), ws_bytes))
 
+
+
+# ---------------------------------------------------------------------------
+# decoding over part of a paged cache
+# ---------------------------------------------------------------------------
+class PreparedOn(Prepared):
+    """A prepared call that keeps its tensors alive and launches on their
+    device, whichever device is current: on the given stream (which must be
+    one of that device) or on that device's current stream."""
+
+    def __init__(self, fn: str, tensors, args):
+        super().__init__(fn, args)
+        self._tensors = [t for t in tensors if t is not None]
+        devices = {t.device for t in self._tensors}
+        if len(devices) != 1:
+            raise ValueError(f"{fn}: all tensors must be on one device")
+        self._device = devices.pop().index
+
+    def __call__(self, stream=None):
+        if stream is None:
+            stream = torch.cuda.current_stream(self._device)
+        elif stream.device_index != self._device:
+            raise ValueError(f"{self.name}: the stream is on another device than the tensors")
+        if torch.cuda.current_device() == self._device:
+            st = self._fn(*self._args, stream.cuda_stream)
+        else:
+            with torch.cuda.device(self._device):
+                st = self._fn(*self._args, stream.cuda_stream)
+        if st != PA_OK:
+            raise PAError(self.name, st)
+
+
+def _rows(block_tables, lens, what):
+    """Number of rows and table width of int32 ``block_tables`` [rows, MB]; every
+    tensor of ``lens`` is int32 [rows]."""
+    _check_int(block_tables, torch.int32, "block_tables")
+    if block_tables.dim() != 2:
+        raise ValueError("block_tables must be [rows, max_blocks_per_seq]")
+    for t, n in zip(lens, what):
+        _check_int(t, torch.int32, n)
+        if t.shape != (block_tables.shape[0],):
+            raise ValueError(f"{n} must be [rows]")
+    return block_tables.shape
+
+
+def _bounds_shape(key_bounds):
+    if key_bounds.dim() != 4 or key_bounds.shape[2] != 2:
+        raise ValueError("key_bounds must be [num_blocks, num_kv_heads, 2, head_dim]")
+    return key_bounds.shape[0], key_bounds.shape[1], key_bounds.shape[3]
+
+
+def prepare_update_key_bounds(key_bounds, k_cache, block_tables, context_lens, new_lens,
+                              max_new_len: int) -> Prepared:
+    """``pa_update_key_bounds`` with its arguments marshalled once."""
+    B, MB = _rows(block_tables, (context_lens, new_lens), ("context_lens", "new_lens"))
+    NB, H_kv, bs, D = k_cache.shape
+    if _bounds_shape(key_bounds) != (NB, H_kv, D):
+        raise ValueError("key_bounds must cover the cache: [num_blocks, num_kv_heads, 2, head_dim]")
+    if key_bounds.dtype != k_cache.dtype:
+        raise TypeError("key_bounds and k_cache must share one dtype")
+    return PreparedOn("pa_update_key_bounds",
+                      (key_bounds, k_cache, block_tables, context_lens, new_lens),
+                      (_p(key_bounds), _p(k_cache), _p(block_tables), _p(context_lens),
+                       _p(new_lens), B, int(max_new_len), H_kv, D, bs, NB, MB, _dt(k_cache)))
+
+
+def pa_update_key_bounds(key_bounds, k_cache, block_tables, context_lens, new_lens,
+                         max_new_len: int, stream=None) -> None:
+    """Refresh ``key_bounds`` [NB, H_kv, 2, D] (elementwise minimum and maximum
+    of each block's valid keys) for the blocks holding the last ``new_lens[b]``
+    tokens of each row."""
+    prepare_update_key_bounds(key_bounds, k_cache, block_tables, context_lens, new_lens,
+                              max_new_len)(stream)
+
+
+def prepare_select_blocks(selected, q, key_bounds, block_tables, context_lens,
+                          max_context_len: int, block_size: int, num_first: int = 0,
+                          num_last: int = 0) -> Prepared:
+    """``pa_select_blocks`` with its arguments marshalled once."""
+    _check_int(selected, torch.int32, "selected")
+    B, MB = _rows(block_tables, (context_lens,), ("context_lens",))
+    NB, H_kv, D = _bounds_shape(key_bounds)
+    if q.dim() != 3 or q.shape[0] != B or q.shape[2] != D:
+        raise ValueError("q must be [num_seqs, num_q_heads, head_dim]")
+    if selected.dim() != 3 or selected.shape[:2] != (B, H_kv):
+        raise ValueError("selected must be [num_seqs, num_kv_heads, max_selected]")
+    if q.dtype != key_bounds.dtype:
+        raise TypeError("q and key_bounds must share one dtype")
+    return PreparedOn("pa_select_blocks", (selected, q, key_bounds, block_tables, context_lens),
+                      (_p(selected), _p(q), _p(key_bounds), _p(block_tables), _p(context_lens),
+                       selected.shape[2], int(num_first), int(num_last), B, q.shape[1], H_kv, D,
+                       int(block_size), NB, MB, int(max_context_len), _dt(q)))
+
+
+def pa_select_blocks(selected, q, key_bounds, block_tables, context_lens, max_context_len: int,
+                     block_size: int, num_first: int = 0, num_last: int = 0,
+                     stream=None) -> None:
+    """List, for each row and K/V head, the ``selected.shape[2]`` blocks whose
+    keys' bounds allow the largest products with the row's queries (the first
+    ``num_first`` and last ``num_last`` blocks always among them), in ascending
+    order, -1 past the last."""
+    prepare_select_blocks(selected, q, key_bounds, block_tables, context_lens, max_context_len,
+                          block_size, num_first, num_last)(stream)
