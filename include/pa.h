@@ -422,6 +422,113 @@ PA_API pa_status pa_select_blocks(int32_t *selected, const void *q, const void *
                                   int block_size, int num_blocks, int max_blocks_per_seq,
                                   int max_context_len, pa_dtype dtype, cudaStream_t stream);
 
+/* pa_decode over listed blocks only: row b's query heads of K/V head h attend
+ * the tokens of the blocks selected[b][h] lists,
+ *   out[b][g] = sum_{j in S} softmax_j(scale * q[b][g] . K_j) V_j,
+ *   S = positions j < context_lens[b] with j / block_size in selected[b][h].
+ *   selected      int32 [num_seqs][num_kv_heads][max_selected], places in row
+ *                 b's table in any order; negative entries are padding. A
+ *                 place listed twice counts its tokens twice. A place at or
+ *                 past ceil(context_lens[b] / block_size), or a block id
+ *                 outside the pool, is skipped and recorded as
+ *                 PA_ERR_BAD_TABLE.
+ *   max_selected  > 0
+ *   partition_size  listed tokens per split (multiple of 16, <= 16384), a full
+ *                 block_size counted for every entry; 0 = automatic; < 0 =
+ *                 never split.
+ *   workspace     >= pa_decode_selected_blocks_workspace_size(...) bytes (may
+ *                 be NULL when that is 0), 256-byte aligned; contents on entry
+ *                 are ignored. Calls that may overlap need one each.
+ * Nothing to attend gives out = 0. Other arguments and errors as for
+ * pa_decode; table entries of blocks that are not listed are never read. */
+PA_API size_t pa_decode_selected_blocks_workspace_size(int num_seqs, int num_q_heads,
+                                                       int num_kv_heads, int head_dim,
+                                                       int block_size, int max_selected,
+                                                       int partition_size);
+PA_API pa_status pa_decode_selected_blocks(void *out, const void *q, const void *k_cache,
+                                           const void *v_cache, const int32_t *block_tables,
+                                           const int32_t *context_lens, const int32_t *selected,
+                                           int max_selected, int num_seqs, int num_q_heads,
+                                           int num_kv_heads, int head_dim, int block_size,
+                                           int num_blocks, int max_blocks_per_seq, float scale,
+                                           int partition_size, void *workspace,
+                                           size_t workspace_bytes, pa_dtype dtype,
+                                           cudaStream_t stream);
+
+/* pa_decode that also adds up each position's attention weight:
+ *   out as pa_decode's (bit for bit), and for j < context_lens[b]
+ *   weights_out[b][h][j] = weights_in[b][h][j]
+ *       + sum over the query heads g of K/V head h of
+ *         softmax_j(scale * q[b][g] . K_j).
+ *   weights_out, weights_in   fp32 [num_seqs][num_kv_heads][weights_stride],
+ *                 weights_stride >= max_context_len. weights_in may be NULL
+ *                 (zeros) or weights_out itself; other overlaps are refused.
+ *                 Positions at and past context_lens[b] are neither read nor
+ *                 written, so a new token's old weight is whatever its place
+ *                 holds: zero it once (pa_evict_tokens zeroes what it frees).
+ *   workspace     >= pa_decode_accumulate_weights_workspace_size(...) bytes,
+ *                 256-byte aligned (it holds every head's scores, 4 bytes per
+ *                 query head and position); contents on entry are ignored.
+ *                 Calls that may overlap need one each.
+ * A token whose block id is outside the pool has no weight. Other arguments
+ * and errors as for pa_decode. */
+PA_API size_t pa_decode_accumulate_weights_workspace_size(int num_seqs, int num_q_heads,
+                                                          int head_dim, int max_context_len,
+                                                          int partition_size);
+PA_API pa_status pa_decode_accumulate_weights(void *out, float *weights_out,
+                                              const float *weights_in, const void *q,
+                                              const void *k_cache, const void *v_cache,
+                                              const int32_t *block_tables,
+                                              const int32_t *context_lens, int num_seqs,
+                                              int num_q_heads, int num_kv_heads, int head_dim,
+                                              int block_size, int num_blocks,
+                                              int max_blocks_per_seq, int max_context_len,
+                                              int weights_stride, float scale,
+                                              int partition_size, void *workspace,
+                                              size_t workspace_bytes, pa_dtype dtype,
+                                              cudaStream_t stream);
+
+/* Cut each row's cache back to `budget` tokens per K/V head, by accumulated
+ * attention weight. Of the n = context_lens[b] positions of row b, K/V head h
+ * keeps min(n, budget): all of them when n <= budget, else the first
+ * num_first, the last num_last and those of largest weights_in[b][h][j]
+ * between them (equal weights: the lower position; a NaN weight ranks above
+ * every number). With p_0 < p_1 < ... the kept positions of (b, h):
+ *   kept_positions[b][h][i] = p_i, then -1        int32 [B][H_kv][budget]
+ *   new_context_lens[b]     = min(n, budget)      int32 [B]
+ *   K and V of position p_i (head h) go to position i of the row's
+ *     destination table: offset i % bs of block dst_block_tables[b][i / bs]
+ *   weights_out[b][h][i] = weights_in[b][h][p_i], and 0 for
+ *     min(n, budget) <= i < n; positions from n on are left as they were.
+ * A kept token keeps its rotary embedding and every other property of its
+ * K/V rows, but no longer its place: windowed calls and further prefill
+ * chunks see places, not the original positions.
+ *   dst_block_tables  int32 [num_seqs][dst_max_blocks_per_seq]; entry
+ *                 (b, i) is block_tables[b][i] itself -- the cache is then
+ *                 compacted in place and the row's later blocks are free
+ *                 afterwards -- or a block that no row of the call reads and
+ *                 no other entry names (a shared prefix's blocks have to be
+ *                 replaced so). Entries past the kept tokens are not read.
+ *                 Other aliasing corrupts the tokens involved.
+ *   weights_in, weights_out  fp32 [num_seqs][num_kv_heads][weights_stride],
+ *                 weights_stride >= max_context_len; the same buffer, or
+ *                 buffers that do not overlap.
+ *   budget        > 0; num_first + num_last <= budget; the destination table
+ *                 must hold min(budget, max_context_len) tokens.
+ *   max_context_len  host-side upper bound of context_lens, as in pa_decode.
+ * new_context_lens and context_lens must not overlap. A token whose source or
+ * destination block id is outside the pool is not moved and recorded as
+ * PA_ERR_BAD_TABLE. Two launches on `stream`. */
+PA_API pa_status pa_evict_tokens(void *k_cache, void *v_cache, float *weights_out,
+                                 const float *weights_in, int32_t *kept_positions,
+                                 int32_t *new_context_lens, const int32_t *block_tables,
+                                 const int32_t *dst_block_tables, const int32_t *context_lens,
+                                 int budget, int num_first, int num_last, int num_seqs,
+                                 int num_kv_heads, int head_dim, int block_size, int num_blocks,
+                                 int max_blocks_per_seq, int dst_max_blocks_per_seq,
+                                 int max_context_len, int weights_stride, pa_dtype dtype,
+                                 cudaStream_t stream);
+
 /* Check block tables and lengths on the device: every entry a row's valid
  * tokens reach must lie in [0, num_blocks), and 0 <= context_lens[r] <=
  * max_blocks_per_seq*block_size. d_scratch is one caller-owned device int32.

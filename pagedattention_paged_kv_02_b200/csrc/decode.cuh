@@ -59,6 +59,23 @@ struct DecodeArgs {
     int P_prefix;      // tokens per prefix partition
     int S_prefix;      // partial slots [0, S_prefix) hold prefix partitions,
                        // [S_prefix, S_max) the private tails' partitions
+    // decode over listed blocks: [B][H_kv][n_listed] places in the row's
+    // table, negative = none
+    const int32_t *selected;
+    int n_listed;
+    // decode that accumulates weights: the scaled base-2 scores
+    // [B][H_q][score_stride], and per partition the maximum and the sum of
+    // the unrounded weights relative to it, [B][H_q][S_max]
+    float *scores, *part_m, *part_l;
+    int score_stride;
+};
+
+// What a split kernel attends to and leaves behind.
+enum class Span {
+    kOwn,       // the row's positions [window start, ctx)
+    kTail,      // the private tail of the shared-prefix decode
+    kListed,    // the tokens of the row's listed blocks, per K/V head
+    kWeighted,  // as kOwn, leaving the scores and their statistics too
 };
 
 // First attended position of a sequence of ctx tokens (the sliding window's
@@ -200,13 +217,74 @@ __device__ __forceinline__ void write_zero_rows(const DecodeArgs &a, int b, int 
     }
 }
 
+// kWeighted: the maximum and the sum of weights of a partition's rows.
+template <int NW, int HT>
+__device__ __forceinline__ void write_statistics(const DecodeArgs &a, const float *red_m,
+                                                 const float *red_u, int b, int h0, int nh,
+                                                 int s) {
+    for (int row = threadIdx.x; row < nh; row += NW * 32) {
+        float M = -INFINITY, U = 0.f;
+#pragma unroll
+        for (int w = 0; w < NW; ++w) M = fmaxf(M, red_m[w * HT + row]);
+        if (M != -INFINITY) {
+#pragma unroll
+            for (int w = 0; w < NW; ++w)
+                U += exp2f(red_m[w * HT + row] - M) * red_u[w * HT + row];
+        }
+        const size_t at = ((size_t)b * a.H_q + h0 + row) * a.S_max + s;
+        a.part_m[at] = M;
+        a.part_l[at] = U;
+    }
+}
+
+// kWeighted: the scores of a chunk whose block is unusable.
+__device__ __forceinline__ void clear_scores(const DecodeArgs &a, float *scores, int t, int nh,
+                                             int lane) {
+    for (int e = lane; e < nh * kChunk; e += 32)
+        scores[(size_t)(e / kChunk) * a.score_stride + t + e % kChunk] = -INFINITY;
+}
+
+// List entries [e0, e0 + n) of (b, kvh) -> their physical ids in tbl[0..n)
+// and their numbers of valid tokens in tbl[P / bs + 2 + 0..n).
+__device__ __forceinline__ void load_listed(const DecodeArgs &a, int b, int kvh, int ctx, int e0,
+                                            int n, int32_t *tbl) {
+    const int32_t *list = a.selected + ((size_t)b * a.H_kv + kvh) * a.n_listed + e0;
+    const int n_blocks = (ctx + a.bs - 1) >> a.bs_shift;
+    for (int i = threadIdx.x; i < n; i += blockDim.x) {
+        const int j = __ldg(list + i);
+        int id = -1, tokens = 0;
+        if (j >= 0 && j < n_blocks) {
+            id = __ldg(a.block_tables + (size_t)b * a.MB + j);
+            tokens = min(a.bs, ctx - (j << a.bs_shift));
+        }
+        if (j >= n_blocks || (j >= 0 && (id < 0 || id >= a.NB))) {
+            flag_error(PA_ERR_BAD_TABLE);
+            id = -1;
+            tokens = 0;
+        }
+        tbl[i] = id;
+        tbl[a.P / a.bs + 2 + i] = tokens;
+    }
+}
+
 // ------------------------------------------------------------------ bf16
-// SHARED: the private-tail pass of the shared-prefix decode. The grid is
+// kTail: the private-tail pass of the shared-prefix decode. The grid is
 // (member x tail partition, KV head [x head tile], group); sequence b of
 // group g attends positions [L, ctx_b) here (L = the group's shared length,
 // decode_prefix.cuh attends [0, L)) and always leaves partials, in slots
 // S_prefix + s, with lse = -inf for a partition that has nothing to attend.
-template <int D, int NW, int NS, bool SHARED = false>
+//
+// kListed: positions count through the row's list of blocks, bs to an entry
+// (position t is offset t % bs of list entry t / bs), and a table slice holds
+// the entries' physical ids and their numbers of valid tokens: all but the
+// row's last block are full, and a negative entry has none. Every partition
+// of every row leaves a partial, lse = -inf where nothing was attended.
+//
+// kWeighted: each chunk's scores also go to `scores` (-inf at tokens of an
+// unusable block), 16 x 4 bytes per query head beside 2 x 16 x D x 2 of K and
+// V; the statistics sum the weights before their rounding to bf16, since the
+// weights are what this form returns.
+template <int D, int NW, int NS, Span SPAN = Span::kOwn>
 __global__ void __launch_bounds__(NW * 32)
     decode_split_bf16(const __grid_constant__ DecodeArgs a, const __grid_constant__ CUtensorMap tmk,
                       const __grid_constant__ CUtensorMap tmv) {
@@ -216,7 +294,11 @@ __global__ void __launch_bounds__(NW * 32)
     constexpr int HALF = kChunk * D * 2;    // bytes of one K (or V) chunk
     constexpr int STAGE = 2 * HALF;
     constexpr int SUBTILE = kChunk * 128;   // one 64-wide swizzled sub-tile
+    constexpr bool SHARED = SPAN == Span::kTail;
+    constexpr bool LISTED = SPAN == Span::kListed;
+    constexpr bool WEIGHTED = SPAN == Span::kWeighted;
     using L = DecodeSmem<NW, NS, STAGE, HT, D>;
+    static_assert(!WEIGHTED || L::kMerge + NW * HT * 4 <= L::kStages, "room for the second sums");
 
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -250,6 +332,12 @@ __global__ void __launch_bounds__(NW * 32)
             wait_for_primary_grid();
             return;
         }
+    } else if constexpr (LISTED) {
+        s = blockIdx.x;
+        b = blockIdx.z;
+        ctx = clamped_ctx(a, b, s == 0 && blockIdx.y == 0 && threadIdx.x == 0);
+        lo = base = 0;
+        n_splits = a.S_max;
     } else {
         s = blockIdx.x;
         b = blockIdx.z;
@@ -264,21 +352,36 @@ __global__ void __launch_bounds__(NW * 32)
         }
     }
     const int tok0 = base + s * a.P;
-    const int tok1 = min(tok0 + a.P, ctx);
+    const int tok1 = min(tok0 + a.P, LISTED ? a.n_listed << a.bs_shift : ctx);
     const int n_chunks = (tok1 - tok0 + kChunk - 1) / kChunk;
     const int lb0 = tok0 >> a.bs_shift;
     const int n_tbl = ((tok1 - 1) >> a.bs_shift) - lb0 + 1;
 
     // table slice of this partition -> shared memory (ids checked once here)
-    const int32_t *row = a.block_tables + (size_t)b * a.MB + lb0;
-    for (int i = threadIdx.x; i < n_tbl; i += NW * 32) {
-        int id = __ldg(row + i);
-        if (id < 0 || id >= a.NB) {
-            flag_error(PA_ERR_BAD_TABLE);
-            id = -1;
+    if constexpr (LISTED) {
+        load_listed(a, b, kvh, ctx, lb0, n_tbl, tbl);
+    } else {
+        const int32_t *row = a.block_tables + (size_t)b * a.MB + lb0;
+        for (int i = threadIdx.x; i < n_tbl; i += NW * 32) {
+            int id = __ldg(row + i);
+            if (id < 0 || id >= a.NB) {
+                flag_error(PA_ERR_BAD_TABLE);
+                id = -1;
+            }
+            tbl[i] = id;
         }
-        tbl[i] = id;
     }
+    // physical block of the chunk at position t, negative when it has no
+    // valid token, and the chunk's number of valid tokens
+    auto block_at = [&](int t) {
+        const int i = (t >> a.bs_shift) - lb0;
+        if (LISTED && (t & (a.bs - 1)) >= tbl[a.P / a.bs + 2 + i]) return -1;
+        return tbl[i];
+    };
+    auto valid_at = [&](int t) {
+        if (!LISTED) return min(kChunk, tok1 - t);
+        return min(kChunk, tbl[a.P / a.bs + 2 + (t >> a.bs_shift) - lb0] - (t & (a.bs - 1)));
+    };
     const uint32_t bar0 = sbase + L::kBars + warp * NS * 8;
     if (lane == 0) {
         for (int st = 0; st < NS; ++st) mbar_init(bar0 + st * 8, 1);
@@ -293,7 +396,7 @@ __global__ void __launch_bounds__(NW * 32)
         const int st = i % NS;
         const uint32_t bar = bar0 + st * 8;
         const int t = tok0 + (warp + i * NW) * kChunk;
-        const int id = tbl[(t >> a.bs_shift) - lb0];
+        const int id = block_at(t);
         if (id < 0) {
             mbar_arrive(bar);  // nothing to load; the chunk is skipped
             return;
@@ -332,6 +435,9 @@ __global__ void __launch_bounds__(NW * 32)
 #pragma unroll
     for (int i = 0; i < DTILES; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
     float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
+    float u0 = 0.f, u1 = 0.f;  // kWeighted: sums of the unrounded weights
+    float *scores = nullptr;
+    if constexpr (WEIGHTED) scores = a.scores + ((size_t)b * a.H_q + h0) * a.score_stride;
     int done = 0;
     bool failed = false;
 
@@ -346,9 +452,9 @@ __global__ void __launch_bounds__(NW * 32)
         }
         done = i + 1;
         const int t = tok0 + (warp + i * NW) * kChunk;
-        const int id = tbl[(t >> a.bs_shift) - lb0];
+        const int id = block_at(t);
         if (id >= 0) {
-            const int valid = min(kChunk, tok1 - t);
+            const int valid = valid_at(t);
             const int first = max(0, lo - t);  // rows before the window start
             const uint32_t kb = stage0 + st * STAGE;
             const uint32_t vb = kb + HALF;
@@ -400,11 +506,34 @@ __global__ void __launch_bounds__(NW * 32)
             const float c0 = exp2f(m0 - mn0), c1 = exp2f(m1 - mn1);
             m0 = mn0;
             m1 = mn1;
+            if constexpr (WEIGHTED) {
+#pragma unroll
+                for (int nt = 0; nt < 2; ++nt) {
+                    const int at = t + nt * 8 + 2 * tig;
+                    if (g < nh)
+                        *reinterpret_cast<float2 *>(scores + (size_t)g * a.score_stride + at) =
+                            make_float2(sc[nt][0], sc[nt][1]);
+                    if (g + 8 < nh)
+                        *reinterpret_cast<float2 *>(scores + (size_t)(g + 8) * a.score_stride +
+                                                    at) = make_float2(sc[nt][2], sc[nt][3]);
+                }
+            }
+#pragma unroll
+            for (int nt = 0; nt < 2; ++nt) {
+                sc[nt][0] = exp2f(sc[nt][0] - mn0);
+                sc[nt][1] = exp2f(sc[nt][1] - mn0);
+                sc[nt][2] = exp2f(sc[nt][2] - mn1);
+                sc[nt][3] = exp2f(sc[nt][3] - mn1);
+            }
             uint32_t pa[4];
-            pa[0] = pack_bf16x2(exp2f(sc[0][0] - mn0), exp2f(sc[0][1] - mn0));
-            pa[1] = pack_bf16x2(exp2f(sc[0][2] - mn1), exp2f(sc[0][3] - mn1));
-            pa[2] = pack_bf16x2(exp2f(sc[1][0] - mn0), exp2f(sc[1][1] - mn0));
-            pa[3] = pack_bf16x2(exp2f(sc[1][2] - mn1), exp2f(sc[1][3] - mn1));
+            pa[0] = pack_bf16x2(sc[0][0], sc[0][1]);
+            pa[1] = pack_bf16x2(sc[0][2], sc[0][3]);
+            pa[2] = pack_bf16x2(sc[1][0], sc[1][1]);
+            pa[3] = pack_bf16x2(sc[1][2], sc[1][3]);
+            if constexpr (WEIGHTED) {
+                u0 = u0 * c0 + (sc[0][0] + sc[0][1] + sc[1][0] + sc[1][1]);
+                u1 = u1 * c1 + (sc[0][2] + sc[0][3] + sc[1][2] + sc[1][3]);
+            }
             // the denominator sums the same rounded weights the numerator uses
             l0 = l0 * c0 + (bf16_lo(pa[0]) + bf16_hi(pa[0]) + bf16_lo(pa[2]) + bf16_hi(pa[2]));
             l1 = l1 * c1 + (bf16_lo(pa[1]) + bf16_hi(pa[1]) + bf16_lo(pa[3]) + bf16_hi(pa[3]));
@@ -433,6 +562,8 @@ __global__ void __launch_bounds__(NW * 32)
                     mma_bf16_16816(o[2 * dp + 1], pa, b2, b3);
                 }
             }
+        } else if constexpr (WEIGHTED) {
+            clear_scores(a, scores, t, nh, lane);
         }
         __syncwarp();
         if (lane == 0 && i + NS < my_n) {
@@ -452,6 +583,12 @@ __global__ void __launch_bounds__(NW * 32)
     l0 += __shfl_xor_sync(0xffffffffu, l0, 2);
     l1 += __shfl_xor_sync(0xffffffffu, l1, 1);
     l1 += __shfl_xor_sync(0xffffffffu, l1, 2);
+    if constexpr (WEIGHTED) {
+        u0 += __shfl_xor_sync(0xffffffffu, u0, 1);
+        u0 += __shfl_xor_sync(0xffffffffu, u0, 2);
+        u1 += __shfl_xor_sync(0xffffffffu, u1, 1);
+        u1 += __shfl_xor_sync(0xffffffffu, u1, 2);
+    }
 
     __syncthreads();  // every warp is done with its stages: reuse them
     constexpr int OS = D + 4;
@@ -463,6 +600,10 @@ __global__ void __launch_bounds__(NW * 32)
         red_m[warp * HT + g + 8] = m1;
         red_l[warp * HT + g] = l0;
         red_l[warp * HT + g + 8] = l1;
+        if constexpr (WEIGHTED) {
+            red_l[(NW + warp) * HT + g] = u0;
+            red_l[(NW + warp) * HT + g + 8] = u1;
+        }
     }
 #pragma unroll
     for (int dt = 0; dt < DTILES; ++dt) {
@@ -479,13 +620,19 @@ __global__ void __launch_bounds__(NW * 32)
         // dependent launch); it completes only after the prefix pass has, so
         // that the merge behind it sees both passes' partials
         wait_for_primary_grid();
-    } else
+    } else {
         decode_epilogue<D, NW, HT, __nv_bfloat16>(a, red_o, red_m, red_l, b, h0, nh, s, n_splits);
+        if constexpr (WEIGHTED)
+            write_statistics<NW, HT>(a, red_m, red_l + NW * HT, b, h0, nh, s);
+    }
 }
 
 // ------------------------------------------------------------------ fp32
-template <int D, int NW, int NS>
+template <int D, int NW, int NS, Span SPAN = Span::kOwn>
 __global__ void __launch_bounds__(NW * 32) decode_split_f32(const __grid_constant__ DecodeArgs a) {
+    static_assert(SPAN != Span::kTail, "no fp32 shared-prefix decode");
+    constexpr bool LISTED = SPAN == Span::kListed;
+    constexpr bool WEIGHTED = SPAN == Span::kWeighted;
     constexpr int HT = kHeadsF32;
     constexpr int VEC = D / 32;          // dims per lane
     constexpr int HALF = kChunk * D * 4;
@@ -507,28 +654,46 @@ __global__ void __launch_bounds__(NW * 32) decode_split_f32(const __grid_constan
 
     allow_dependent_launch();
     const int ctx = clamped_ctx(a, b, s == 0 && blockIdx.y == 0 && threadIdx.x == 0);
-    const int lo = window_lo(a, ctx), base = span_base(a, ctx);
-    const int n_splits = (ctx - base + a.P - 1) / a.P;
-    if (s >= (n_splits > 0 ? n_splits : 1)) return;
-    if (ctx == 0) {
-        write_zero_rows<D, float>(a, b, h0, nh);
-        return;
+    const int lo = LISTED ? 0 : window_lo(a, ctx), base = LISTED ? 0 : span_base(a, ctx);
+    const int n_splits = LISTED ? a.S_max : (ctx - base + a.P - 1) / a.P;
+    if (!LISTED) {
+        if (s >= (n_splits > 0 ? n_splits : 1)) return;
+        if (ctx == 0) {
+            write_zero_rows<D, float>(a, b, h0, nh);
+            return;
+        }
     }
     const int tok0 = base + s * a.P;
-    const int tok1 = min(tok0 + a.P, ctx);
+    const int tok1 = min(tok0 + a.P, LISTED ? a.n_listed << a.bs_shift : ctx);
     const int n_chunks = (tok1 - tok0 + kChunk - 1) / kChunk;
     const int lb0 = tok0 >> a.bs_shift;
     const int n_tbl = ((tok1 - 1) >> a.bs_shift) - lb0 + 1;
 
-    const int32_t *row = a.block_tables + (size_t)b * a.MB + lb0;
-    for (int i = threadIdx.x; i < n_tbl; i += NW * 32) {
-        int id = __ldg(row + i);
-        if (id < 0 || id >= a.NB) {
-            flag_error(PA_ERR_BAD_TABLE);
-            id = -1;
+    // table slice of this partition -> shared memory (ids checked once here)
+    if constexpr (LISTED) {
+        load_listed(a, b, kvh, ctx, lb0, n_tbl, tbl);
+    } else {
+        const int32_t *row = a.block_tables + (size_t)b * a.MB + lb0;
+        for (int i = threadIdx.x; i < n_tbl; i += NW * 32) {
+            int id = __ldg(row + i);
+            if (id < 0 || id >= a.NB) {
+                flag_error(PA_ERR_BAD_TABLE);
+                id = -1;
+            }
+            tbl[i] = id;
         }
-        tbl[i] = id;
     }
+    // physical block of the chunk at position t, negative when it has no
+    // valid token, and the chunk's number of valid tokens
+    auto block_at = [&](int t) {
+        const int i = (t >> a.bs_shift) - lb0;
+        if (LISTED && (t & (a.bs - 1)) >= tbl[a.P / a.bs + 2 + i]) return -1;
+        return tbl[i];
+    };
+    auto valid_at = [&](int t) {
+        if (!LISTED) return min(kChunk, tok1 - t);
+        return min(kChunk, tbl[a.P / a.bs + 2 + (t >> a.bs_shift) - lb0] - (t & (a.bs - 1)));
+    };
     const uint32_t bar0 = sbase + L::kBars + warp * NS * 8;
     if (lane == 0) {
         for (int st = 0; st < NS; ++st) mbar_init(bar0 + st * 8, 1);
@@ -545,7 +710,7 @@ __global__ void __launch_bounds__(NW * 32) decode_split_f32(const __grid_constan
         const int st = i % NS;
         const uint32_t bar = bar0 + st * 8;
         const int t = tok0 + (warp + i * NW) * kChunk;
-        const int id = tbl[(t >> a.bs_shift) - lb0];
+        const int id = block_at(t);
         if (id < 0) {
             mbar_arrive(bar);
             return;
@@ -573,6 +738,8 @@ __global__ void __launch_bounds__(NW * 32) decode_split_f32(const __grid_constan
             lrow[g] = 0.f;
         }
     }
+    float *scores = nullptr;
+    if constexpr (WEIGHTED) scores = a.scores + ((size_t)b * a.H_q + h0) * a.score_stride;
     int done = 0;
     bool failed = false;
     for (int i = 0; i < my_n; ++i) {
@@ -586,9 +753,9 @@ __global__ void __launch_bounds__(NW * 32) decode_split_f32(const __grid_constan
         }
         done = i + 1;
         const int t = tok0 + (warp + i * NW) * kChunk;
-        const int id = tbl[(t >> a.bs_shift) - lb0];
+        const int id = block_at(t);
         if (id >= 0) {
-            const int valid = min(kChunk, tok1 - t);
+            const int valid = valid_at(t);
             const int first = max(0, lo - t);
             const float *ks = reinterpret_cast<const float *>(smem + warp * NS * STAGE + st * STAGE);
             const float *vs = ks + kChunk * D;
@@ -606,6 +773,7 @@ __global__ void __launch_bounds__(NW * 32) decode_split_f32(const __grid_constan
 #pragma unroll
                         for (int v = 0; v < VEC; ++v) dot = fmaf(qv[g][v], kk[v], dot);
                         const float sc = warp_sum(dot) * a.scale_log2;
+                        if (WEIGHTED && lane == 0) scores[(size_t)g * a.score_stride + t + j] = sc;
                         const float mn = fmaxf(mrow[g], sc);
                         const float c = exp2f(mrow[g] - mn);
                         const float p = exp2f(sc - mn);
@@ -616,6 +784,8 @@ __global__ void __launch_bounds__(NW * 32) decode_split_f32(const __grid_constan
                     }
                 }
             }
+        } else if constexpr (WEIGHTED) {
+            clear_scores(a, scores, t, nh, lane);
         }
         __syncwarp();
         if (lane == 0 && i + NS < my_n) {
@@ -646,6 +816,7 @@ __global__ void __launch_bounds__(NW * 32) decode_split_f32(const __grid_constan
     }
     __syncthreads();
     decode_epilogue<D, NW, HT, float>(a, red_o, red_m, red_l, b, h0, nh, s, n_splits);
+    if constexpr (WEIGHTED) write_statistics<NW, HT>(a, red_m, red_l, b, h0, nh, s);
 }
 
 }  // namespace pa

@@ -27,9 +27,9 @@ namespace pa {
 // walking the partitions in order; heads with one partition cost a warp a
 // length read.
 //
-// SHARED (the shared-prefix decode): every one of the S_max slots of every
-// (sequence, head) was written -- prefix partitions, then the private tail's
-// -- and a slot with lse = -inf (nothing attended) has no partial output:
+// SHARED (the shared-prefix decode, and the decode over listed blocks): every
+// one of the S_max slots of every (sequence, head) was written -- prefix
+// partitions, then the private tail's, or the list's partitions -- and a slot with lse = -inf (nothing attended) has no partial output:
 // its weight is zero and its output is never read.
 constexpr int kWarpMergeMax = 16;
 

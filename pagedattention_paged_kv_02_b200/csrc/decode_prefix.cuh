@@ -10,7 +10,7 @@
 // log-sum-exp): positions [0, L), the same K/V for every sequence of the
 // group, and positions [L, ctx_b), the sequence's own. This kernel computes
 // the first part for all sequences of a group at once; the private tails go
-// through decode_split_bf16<..., SHARED = true> and the merge kernel
+// through decode_split_bf16<..., Span::kTail> and the merge kernel
 // (decode_merge.cuh) combines the partials.
 //
 // Work decomposition: one CTA per (prefix partition, KV head x row tile,

@@ -1,0 +1,103 @@
+// decode_weights.cuh -- attention weights of a decode step, added up per
+// position: the second kernel of the decode that accumulates weights.
+//
+// The split kernel (decode.cuh, Span::kWeighted) left every query head's
+// scaled base-2 scores s_j and, per partition, the maximum m and the sum u of
+// 2^(s_j - m) in 32 bits. Over the partitions of a head
+//     M = max m,   U = sum u 2^(m - M),
+// and a position's weight is p_j = 2^(s_j - M) / U. For each K/V head h
+//     weights_out[b][h][j] = weights_in[b][h][j] + sum over the group of p_j
+// (page "字节跳动 AI Infra (2)", KV table, H2O row: the tokens to keep are the
+// ones attended to most). M and U are kept apart rather than as a logarithm:
+// s_j - M is then the difference of two scores, whose rounding does not grow
+// with log U.
+//
+// One CTA per (tile of 1024 positions, K/V head, row), four positions per
+// thread; the statistics of the head's group are put together by the CTA's
+// warps first. Reads 4 bytes per query head and 4 per K/V head and position
+// (the scores mostly from L2), writes 4. Heads are added in order: the result
+// does not depend on timing.
+#pragma once
+
+#include "decode.cuh"
+
+namespace pa {
+
+constexpr int kWeightThreads = 256;
+constexpr int kWeightTile = 4 * kWeightThreads;
+constexpr int kWeightHeads = 64;  // heads whose statistics a CTA holds at a time
+
+struct WeightArgs {
+    float *weights_out;
+    const float *weights_in;  // may be null (zeros) or weights_out
+    long long stride;         // positions per (row, K/V head) of both
+    int vec;                  // rows of weights and scores allow 16-byte accesses
+};
+
+__global__ void __launch_bounds__(kWeightThreads)
+    decode_weights_kernel(const __grid_constant__ DecodeArgs a,
+                          const __grid_constant__ WeightArgs w) {
+    __shared__ float top[kWeightHeads], inv[kWeightHeads];
+    // every CTA waits: nothing behind this grid can run before the split
+    // kernel has finished
+    wait_for_primary_grid();
+    const int h = blockIdx.y, b = blockIdx.z;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int ctx = clamped_ctx(a, b, false);
+    const int t0 = blockIdx.x * kWeightTile;
+    if (t0 >= ctx) return;
+    const int n_splits = (ctx + a.P - 1) / a.P;
+    const int t = t0 + 4 * threadIdx.x;
+    float sum[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int g0 = 0; g0 < a.group; g0 += kWeightHeads) {
+        const int n = min(kWeightHeads, a.group - g0);
+        const size_t head = (size_t)b * a.H_q + (size_t)h * a.group + g0;
+        __syncthreads();  // the previous heads' statistics have been used
+        for (int g = warp; g < n; g += kWeightThreads / 32) {
+            const float *pm = a.part_m + (head + g) * a.S_max;
+            const float *pl = a.part_l + (head + g) * a.S_max;
+            float M = -INFINITY, U = 0.f;
+            for (int s = lane; s < n_splits; s += 32) M = fmaxf(M, pm[s]);
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+            if (M != -INFINITY)
+                for (int s = lane; s < n_splits; s += 32) U += pl[s] * exp2f(pm[s] - M);
+            U = warp_sum(U);
+            if (lane == 0) {
+                top[g] = M;
+                inv[g] = U == 0.f ? 0.f : 1.f / U;  // no usable token: no weight
+            }
+        }
+        __syncthreads();
+        if (t >= ctx) continue;
+        const float *sc = a.scores + head * a.score_stride + t;
+#pragma unroll 4
+        for (int g = 0; g < n; ++g) {
+            // whole 16-token chunks of scores were written
+            const float4 x = *reinterpret_cast<const float4 *>(sc + (size_t)g * a.score_stride);
+            const float M = top[g], r = inv[g];
+            if (r == 0.f) continue;
+            sum[0] = fmaf(exp2f(x.x - M), r, sum[0]);
+            sum[1] = fmaf(exp2f(x.y - M), r, sum[1]);
+            sum[2] = fmaf(exp2f(x.z - M), r, sum[2]);
+            sum[3] = fmaf(exp2f(x.w - M), r, sum[3]);
+        }
+    }
+    if (t >= ctx) return;
+    const size_t at = (size_t)((long long)b * a.H_kv + h) * w.stride + t;
+    if (w.vec && t + 4 <= ctx) {
+        if (w.weights_in) {
+            const float4 x = *reinterpret_cast<const float4 *>(w.weights_in + at);
+            sum[0] += x.x, sum[1] += x.y, sum[2] += x.z, sum[3] += x.w;
+        }
+        *reinterpret_cast<float4 *>(w.weights_out + at) =
+            make_float4(sum[0], sum[1], sum[2], sum[3]);
+    } else {
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+            if (t + u < ctx)
+                w.weights_out[at + u] = (w.weights_in ? w.weights_in[at + u] : 0.f) + sum[u];
+    }
+}
+
+}  // namespace pa

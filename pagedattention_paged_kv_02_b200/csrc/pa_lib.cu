@@ -26,6 +26,8 @@
 #include "blocks.cuh"
 #include "key_bounds.cuh"
 #include "select_blocks.cuh"
+#include "decode_weights.cuh"
+#include "evict.cuh"
 
 namespace {
 
@@ -112,24 +114,31 @@ constexpr int kDecodeWarps = 4;
 constexpr int kDecodeStages = 2;
 constexpr int kQ8Tokens = 32;
 
-template <int D, int NW, int NS>
+// Bytes of a split CTA's table slice: block ids, and for listed blocks their
+// numbers of valid tokens.
+template <Span SPAN>
+size_t slice_bytes(const DecodeArgs &a) {
+    return ((size_t)a.P / a.bs + 2) * 4 * (SPAN == Span::kListed ? 2 : 1);
+}
+
+template <int D, int NW, int NS, Span SPAN = Span::kOwn>
 pa_status launch_decode_bf16(const DecodeArgs &a, const CUtensorMap &mk, const CUtensorMap &mv,
                              dim3 grid, cudaStream_t st) {
     constexpr int STAGE = 2 * kChunk * D * 2;
     using L = DecodeSmem<NW, NS, STAGE, kHeadsBf16, D>;
-    const size_t smem = 1024 + L::kTable + ((size_t)a.P / a.bs + 2) * 4;
-    auto k = decode_split_bf16<D, NW, NS>;
+    const size_t smem = 1024 + L::kTable + slice_bytes<SPAN>(a);
+    auto k = decode_split_bf16<D, NW, NS, SPAN>;
     if (set_smem(k, smem) != cudaSuccess) return PA_ERR_CUDA;
     k<<<grid, NW * 32, smem, st>>>(a, mk, mv);
     return launch_status();
 }
 
-template <int D, int NW, int NS>
+template <int D, int NW, int NS, Span SPAN = Span::kOwn>
 pa_status launch_decode_f32(const DecodeArgs &a, dim3 grid, cudaStream_t st) {
     constexpr int STAGE = 2 * kChunk * D * 4;
     using L = DecodeSmem<NW, NS, STAGE, kHeadsF32, D>;
-    const size_t smem = 1024 + L::kTable + ((size_t)a.P / a.bs + 2) * 4;
-    auto k = decode_split_f32<D, NW, NS>;
+    const size_t smem = 1024 + L::kTable + slice_bytes<SPAN>(a);
+    auto k = decode_split_f32<D, NW, NS, SPAN>;
     if (set_smem(k, smem) != cudaSuccess) return PA_ERR_CUDA;
     k<<<grid, NW * 32, smem, st>>>(a);
     return launch_status();
@@ -268,7 +277,7 @@ pa_status launch_tail(const DecodeArgs &a, const CUtensorMap &mk, const CUtensor
     constexpr int STAGE = 2 * kChunk * D * 2;
     using L = DecodeSmem<kDecodeWarps, kDecodeStages, STAGE, kHeadsBf16, D>;
     const size_t smem = 1024 + L::kTable + ((size_t)a.P / a.bs + 2) * 4;
-    auto k = decode_split_bf16<D, kDecodeWarps, kDecodeStages, true>;
+    auto k = decode_split_bf16<D, kDecodeWarps, kDecodeStages, Span::kTail>;
     if (set_smem(k, smem) != cudaSuccess) return PA_ERR_CUDA;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];

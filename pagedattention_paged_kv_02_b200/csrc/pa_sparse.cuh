@@ -52,6 +52,108 @@ int cluster_size(long long rows, long long items, int grain) {
     return cs;
 }
 
+// KV tokens per partition of a decode over n_listed blocks, or -1. Automatic:
+// up to 1024 tokens, halved while the grid has fewer than two CTAs per SM and
+// a partition keeps more than 128 tokens.
+int listed_partition(int n_listed, int bs, long long rows, int partition_size) {
+    const long long total = (long long)n_listed * bs;
+    if (total <= 0 || total > 0x7fffffffLL) return -1;
+    if (partition_size > 0)
+        return partition_size % kChunk != 0 || partition_size > kMaxPartition ? -1 : partition_size;
+    if (partition_size < 0) return total <= kMaxPartition ? (int)total : -1;
+    int P = total <= 1024 ? (int)total : 1024;
+    while (rows * ((total + P - 1) / P) < 2 * 148 && P > 128) P = round16(P / 2);
+    return P;
+}
+
+long long listed_rows(int num_seqs, int num_q_heads, int num_kv_heads) {
+    const int group = num_q_heads / num_kv_heads;
+    return (long long)num_seqs * num_kv_heads * ((group + kHeadsBf16 - 1) / kHeadsBf16);
+}
+
+// Partials of S partitions for every (row, query head): outputs, then lse.
+size_t partial_bytes(int B, int H_q, int D, long long S) {
+    if (S <= 1) return 0;
+    const size_t o = (size_t)B * H_q * S * D * sizeof(float);
+    const size_t l = (size_t)B * H_q * S * sizeof(float);
+    return (o + 255) / 256 * 256 + (l + 255) / 256 * 256;
+}
+
+// What the weight-accumulating decode adds to pa_decode's partials: two
+// statistics per partition, then the scores.
+size_t statistics_bytes(int B, int H_q, long long S) {
+    return ((size_t)B * H_q * S * sizeof(float) + 255) / 256 * 256;
+}
+size_t score_bytes(int B, int H_q, int max_ctx) {
+    return ((size_t)B * H_q * round16(max_ctx) * sizeof(float) + 255) / 256 * 256;
+}
+
+// Fills what every decode form shares and launches the split kernel.
+struct DecodeShape {
+    int num_seqs, num_q_heads, num_kv_heads, head_dim, block_size, num_blocks, max_blocks_per_seq;
+    pa_dtype dtype;
+};
+
+void fill_decode(DecodeArgs &a, const DecodeShape &s, void *out, const void *q,
+                 const void *k_cache, const void *v_cache, const int32_t *block_tables,
+                 const int32_t *context_lens, float scale, int P, long long S, void *workspace) {
+    std::memset(&a, 0, sizeof(a));
+    a.out = out;
+    a.q = q;
+    a.k_cache = k_cache;
+    a.v_cache = v_cache;
+    a.block_tables = block_tables;
+    a.context_lens = context_lens;
+    if (S > 1) {
+        a.part_o = static_cast<float *>(workspace);
+        a.part_lse = reinterpret_cast<float *>(
+            static_cast<char *>(workspace) +
+            ((size_t)s.num_seqs * s.num_q_heads * S * s.head_dim * 4 + 255) / 256 * 256);
+    }
+    a.num_seqs = s.num_seqs;
+    a.H_q = s.num_q_heads;
+    a.H_kv = s.num_kv_heads;
+    a.group = s.num_q_heads / s.num_kv_heads;
+    a.bs = s.block_size;
+    a.bs_shift = __builtin_ctz((unsigned)s.block_size);
+    a.NB = s.num_blocks;
+    a.MB = s.max_blocks_per_seq;
+    a.P = P;
+    a.S_max = (int)S;
+    const int ht = s.dtype == PA_BF16 ? kHeadsBf16 : kHeadsF32;
+    a.n_htiles = (a.group + ht - 1) / ht;
+    a.scale_log2 = scale * 1.4426950408889634f;
+    a.timeout_ns = kWaitTimeoutNs;
+}
+
+template <Span SPAN>
+pa_status launch_split(const DecodeArgs &a, const DecodeShape &s, cudaStream_t stream) {
+    const dim3 grid((unsigned)a.S_max, (unsigned)(a.H_kv * a.n_htiles), (unsigned)a.num_seqs);
+    if (s.dtype == PA_BF16) {
+        CUtensorMap mk, mv;
+        if (!encode_cache_map(&mk, a.k_cache, a.NB, a.H_kv, a.bs, s.head_dim, kChunk) ||
+            !encode_cache_map(&mv, a.v_cache, a.NB, a.H_kv, a.bs, s.head_dim, kChunk))
+            return PA_ERR_CUDA;
+        return s.head_dim == 128
+                   ? launch_decode_bf16<128, kDecodeWarps, kDecodeStages, SPAN>(a, mk, mv, grid,
+                                                                                stream)
+                   : launch_decode_bf16<64, kDecodeWarps, kDecodeStages, SPAN>(a, mk, mv, grid,
+                                                                               stream);
+    }
+    return s.head_dim == 128
+               ? launch_decode_f32<128, kDecodeWarps, kDecodeStages, SPAN>(a, grid, stream)
+               : launch_decode_f32<64, kDecodeWarps, kDecodeStages, SPAN>(a, grid, stream);
+}
+
+// Checks of the arguments that both decode forms below share, in pa_decode's
+// order; num_seqs == 0 has been dealt with.
+bool decode_pointers_ok(const void *out, const void *q, const void *k_cache, const void *v_cache,
+                        const void *block_tables, const void *context_lens) {
+    return out && q && k_cache && v_cache && block_tables && context_lens && aligned(out, 16) &&
+           aligned(q, 16) && aligned(k_cache, 16) && aligned(v_cache, 16) &&
+           aligned(block_tables, 4) && aligned(context_lens, 4);
+}
+
 }  // namespace
 
 extern "C" {
@@ -158,6 +260,223 @@ pa_status pa_select_blocks(int32_t *selected, const void *q, const void *key_bou
                                             cs, smem, stream)
                            : launch_cluster(select_blocks_kernel<64, float>, a, grid, kSelThreads,
                                             cs, smem, stream);
+}
+
+size_t pa_decode_selected_blocks_workspace_size(int num_seqs, int num_q_heads, int num_kv_heads,
+                                                int head_dim, int block_size, int max_selected,
+                                                int partition_size) {
+    if (num_seqs < 0 || num_q_heads <= 0 || num_kv_heads <= 0 || head_dim <= 0 ||
+        num_q_heads % num_kv_heads != 0 || block_size <= 0 || max_selected <= 0)
+        return 0;
+    const int P = listed_partition(max_selected, block_size,
+                                   listed_rows(num_seqs, num_q_heads, num_kv_heads),
+                                   partition_size);
+    if (P <= 0) return 0;
+    return partial_bytes(num_seqs, num_q_heads, head_dim,
+                         ((long long)max_selected * block_size + P - 1) / P);
+}
+
+pa_status pa_decode_selected_blocks(void *out, const void *q, const void *k_cache,
+                                    const void *v_cache, const int32_t *block_tables,
+                                    const int32_t *context_lens, const int32_t *selected,
+                                    int max_selected, int num_seqs, int num_q_heads,
+                                    int num_kv_heads, int head_dim, int block_size,
+                                    int num_blocks, int max_blocks_per_seq, float scale,
+                                    int partition_size, void *workspace,
+                                    size_t workspace_bytes_given, pa_dtype dtype,
+                                    cudaStream_t stream) {
+    pa_status st = check_cache_shape(num_seqs, num_kv_heads, head_dim, block_size, num_blocks,
+                                     max_blocks_per_seq, dtype);
+    if (st != PA_OK) return st;
+    if (num_q_heads <= 0 || max_selected <= 0 || !std::isfinite(scale)) return PA_ERR_INVALID_ARG;
+    if (num_q_heads % num_kv_heads != 0) return PA_ERR_UNSUPPORTED;
+    const int P = listed_partition(max_selected, block_size,
+                                   listed_rows(num_seqs, num_q_heads, num_kv_heads),
+                                   partition_size);
+    if (P <= 0) return partition_size > 0 ? PA_ERR_INVALID_ARG : PA_ERR_UNSUPPORTED;
+    if (num_seqs == 0) return PA_OK;
+    if (!decode_pointers_ok(out, q, k_cache, v_cache, block_tables, context_lens) || !selected ||
+        !aligned(selected, 4))
+        return PA_ERR_INVALID_ARG;
+    const long long S = ((long long)max_selected * block_size + P - 1) / P;
+    const size_t need = partial_bytes(num_seqs, num_q_heads, head_dim, S);
+    if (need > 0 && (!workspace || workspace_bytes_given < need || !aligned(workspace, 256)))
+        return PA_ERR_WORKSPACE;
+    const DecodeShape shape{num_seqs,   num_q_heads, num_kv_heads,       head_dim,
+                            block_size, num_blocks,  max_blocks_per_seq, dtype};
+    DecodeArgs a;
+    fill_decode(a, shape, out, q, k_cache, v_cache, block_tables, context_lens, scale, P, S,
+                workspace);
+    if ((long long)num_kv_heads * a.n_htiles > 65535) return PA_ERR_UNSUPPORTED;
+    a.max_ctx = max_blocks_per_seq * block_size;
+    a.selected = selected;
+    a.n_listed = max_selected;
+    st = launch_split<Span::kListed>(a, shape, stream);
+    if (st != PA_OK || S <= 1) return st;
+    if (dtype == PA_BF16)
+        return head_dim == 128 ? launch_reduce<128, __nv_bfloat16, true>(a, stream)
+                               : launch_reduce<64, __nv_bfloat16, true>(a, stream);
+    return head_dim == 128 ? launch_reduce<128, float, true>(a, stream)
+                           : launch_reduce<64, float, true>(a, stream);
+}
+
+size_t pa_decode_accumulate_weights_workspace_size(int num_seqs, int num_q_heads, int head_dim,
+                                                   int max_context_len, int partition_size) {
+    const int P = partition_tokens(max_context_len, partition_size);
+    if (P <= 0 || num_seqs <= 0 || num_q_heads <= 0 || head_dim <= 0 || max_context_len == 0)
+        return 0;
+    const long long S = ((long long)max_context_len + P - 1) / P;
+    return partial_bytes(num_seqs, num_q_heads, head_dim, S) +
+           2 * statistics_bytes(num_seqs, num_q_heads, S) +
+           score_bytes(num_seqs, num_q_heads, max_context_len);
+}
+
+pa_status pa_decode_accumulate_weights(void *out, float *weights_out, const float *weights_in,
+                                       const void *q, const void *k_cache, const void *v_cache,
+                                       const int32_t *block_tables, const int32_t *context_lens,
+                                       int num_seqs, int num_q_heads, int num_kv_heads,
+                                       int head_dim, int block_size, int num_blocks,
+                                       int max_blocks_per_seq, int max_context_len,
+                                       int weights_stride, float scale, int partition_size,
+                                       void *workspace, size_t workspace_bytes_given,
+                                       pa_dtype dtype, cudaStream_t stream) {
+    pa_status st = check_cache_shape(num_seqs, num_kv_heads, head_dim, block_size, num_blocks,
+                                     max_blocks_per_seq, dtype);
+    if (st != PA_OK) return st;
+    if (num_q_heads <= 0 || max_context_len < 0 || !std::isfinite(scale)) return PA_ERR_INVALID_ARG;
+    if (num_q_heads % num_kv_heads != 0) return PA_ERR_UNSUPPORTED;
+    if ((long long)max_context_len > (long long)max_blocks_per_seq * block_size ||
+        weights_stride < max_context_len)
+        return PA_ERR_INVALID_ARG;
+    const int P = partition_tokens(max_context_len, partition_size);
+    if (P <= 0) return partition_size > 0 ? PA_ERR_INVALID_ARG : PA_ERR_UNSUPPORTED;
+    if (num_seqs == 0) return PA_OK;
+    if (!decode_pointers_ok(out, q, k_cache, v_cache, block_tables, context_lens) ||
+        !weights_out || !aligned(weights_out, 4) || !aligned(weights_in, 4))
+        return PA_ERR_INVALID_ARG;
+    // the new weights go over the old ones, or elsewhere; never half over them
+    const size_t span = (size_t)num_seqs * num_kv_heads * weights_stride;
+    if (weights_in && weights_in != weights_out && weights_in < weights_out + span &&
+        weights_out < weights_in + span)
+        return PA_ERR_INVALID_ARG;
+    const size_t need = pa_decode_accumulate_weights_workspace_size(
+        num_seqs, num_q_heads, head_dim, max_context_len, partition_size);
+    if (need > 0 && (!workspace || workspace_bytes_given < need || !aligned(workspace, 256)))
+        return PA_ERR_WORKSPACE;
+    const long long S = std::max<long long>(1, ((long long)max_context_len + P - 1) / P);
+    const DecodeShape shape{num_seqs,   num_q_heads, num_kv_heads,       head_dim,
+                            block_size, num_blocks,  max_blocks_per_seq, dtype};
+    DecodeArgs a;
+    fill_decode(a, shape, out, q, k_cache, v_cache, block_tables, context_lens, scale, P, S,
+                workspace);
+    if ((long long)num_kv_heads * a.n_htiles > 65535) return PA_ERR_UNSUPPORTED;
+    a.max_ctx = max_context_len;
+    char *ws = static_cast<char *>(workspace) + partial_bytes(num_seqs, num_q_heads, head_dim, S);
+    a.part_m = reinterpret_cast<float *>(ws);
+    a.part_l = reinterpret_cast<float *>(ws + statistics_bytes(num_seqs, num_q_heads, S));
+    a.scores = reinterpret_cast<float *>(ws + 2 * statistics_bytes(num_seqs, num_q_heads, S));
+    a.score_stride = round16(max_context_len);
+    st = launch_split<Span::kWeighted>(a, shape, stream);
+    if (st != PA_OK || max_context_len == 0) return st;
+
+    WeightArgs w;
+    w.weights_out = weights_out;
+    w.weights_in = weights_in;
+    w.stride = weights_stride;
+    w.vec = weights_stride % 4 == 0 && aligned(weights_out, 16) && aligned(weights_in, 16);
+    // programmatic dependent of the split kernel; the merge behind it starts
+    // when it has finished
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    cfg.stream = stream;
+    cfg.gridDim = dim3((unsigned)((max_context_len + kWeightTile - 1) / kWeightTile),
+                       (unsigned)num_kv_heads, (unsigned)num_seqs);
+    cfg.blockDim = dim3(kWeightThreads);
+    if (cudaLaunchKernelEx(&cfg, decode_weights_kernel, a, w) != cudaSuccess) {
+        cudaGetLastError();
+        return PA_ERR_CUDA;
+    }
+    if (S <= 1) return launch_status();
+    if (dtype == PA_BF16)
+        return head_dim == 128 ? launch_reduce<128, __nv_bfloat16>(a, stream)
+                               : launch_reduce<64, __nv_bfloat16>(a, stream);
+    return head_dim == 128 ? launch_reduce<128, float>(a, stream)
+                           : launch_reduce<64, float>(a, stream);
+}
+
+pa_status pa_evict_tokens(void *k_cache, void *v_cache, float *weights_out,
+                          const float *weights_in, int32_t *kept_positions,
+                          int32_t *new_context_lens, const int32_t *block_tables,
+                          const int32_t *dst_block_tables, const int32_t *context_lens,
+                          int budget, int num_first, int num_last, int num_seqs,
+                          int num_kv_heads, int head_dim, int block_size, int num_blocks,
+                          int max_blocks_per_seq, int dst_max_blocks_per_seq,
+                          int max_context_len, int weights_stride, pa_dtype dtype,
+                          cudaStream_t stream) {
+    const pa_status st = check_cache_shape(num_seqs, num_kv_heads, head_dim, block_size,
+                                           num_blocks, max_blocks_per_seq, dtype);
+    if (st != PA_OK) return st;
+    if (budget <= 0 || num_first < 0 || num_last < 0 ||
+        (long long)num_first + num_last > budget || dst_max_blocks_per_seq <= 0 ||
+        max_context_len < 0 || weights_stride < max_context_len)
+        return PA_ERR_INVALID_ARG;
+    if ((long long)max_context_len > (long long)max_blocks_per_seq * block_size ||
+        std::min(budget, max_context_len) > (long long)dst_max_blocks_per_seq * block_size)
+        return PA_ERR_INVALID_ARG;
+    if (num_seqs == 0) return PA_OK;
+    if (!k_cache || !v_cache || !weights_out || !weights_in || !kept_positions ||
+        !new_context_lens || !block_tables || !dst_block_tables || !context_lens)
+        return PA_ERR_INVALID_ARG;
+    if (!aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(weights_out, 4) ||
+        !aligned(weights_in, 4) || !aligned(kept_positions, 4) || !aligned(new_context_lens, 4) ||
+        !aligned(block_tables, 4) || !aligned(dst_block_tables, 4) || !aligned(context_lens, 4))
+        return PA_ERR_INVALID_ARG;
+    // both kernels read the old lengths while the first writes the new ones
+    if (new_context_lens < context_lens + num_seqs && context_lens < new_context_lens + num_seqs)
+        return PA_ERR_INVALID_ARG;
+    const size_t span = (size_t)num_seqs * num_kv_heads * weights_stride;
+    if (weights_in != weights_out && weights_in < weights_out + span &&
+        weights_out < weights_in + span)
+        return PA_ERR_INVALID_ARG;
+    EvictArgs a;
+    a.k_cache = static_cast<char *>(k_cache);
+    a.v_cache = static_cast<char *>(v_cache);
+    a.weights_out = weights_out;
+    a.weights_in = weights_in;
+    a.kept = kept_positions;
+    a.new_lens = new_context_lens;
+    a.block_tables = block_tables;
+    a.dst_tables = dst_block_tables;
+    a.context_lens = context_lens;
+    a.stride = weights_stride;
+    a.H_kv = num_kv_heads;
+    a.bs = block_size;
+    a.bs_shift = __builtin_ctz((unsigned)block_size);
+    a.NB = num_blocks;
+    a.MB = max_blocks_per_seq;
+    a.dst_MB = dst_max_blocks_per_seq;
+    a.max_ctx = max_context_len;
+    a.budget = budget;
+    a.first = num_first;
+    a.last = num_last;
+    a.row_bytes = head_dim * (dtype == PA_BF16 ? 2 : 4);
+    const long long rows = (long long)num_seqs * num_kv_heads;
+    const int cs = cluster_size(rows, max_context_len, 2048);
+    pa_status r = launch_cluster(evict_select_kernel, a,
+                                 dim3((unsigned)cs, (unsigned)num_kv_heads, (unsigned)num_seqs),
+                                 kSelThreads, cs, 0, stream);
+    if (r != PA_OK) return r;
+    // narrower columns, down to 64 bytes, until there are four CTAs per SM
+    a.columns = 1;
+    while (a.row_bytes / a.columns > 64 && 2 * rows * a.columns < 4 * 148) a.columns *= 2;
+    evict_move_kernel<<<dim3((unsigned)(2 * a.columns + 1), (unsigned)num_kv_heads,
+                             (unsigned)num_seqs),
+                        kMoveThreads, 0, stream>>>(a);
+    return launch_status();
 }
 
 }  // extern "C"

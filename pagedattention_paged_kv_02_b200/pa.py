@@ -29,7 +29,10 @@ EXPORTS = ("pa_reshape_and_cache", "pa_decode_workspace_size", "pa_decode_partit
            "pa_reshape_and_cache_fp8", "pa_decode_fp8", "pa_decode_sliding_window",
            "pa_prefill_chunk_sliding_window", "pa_reshape_and_cache_int8", "pa_decode_int8",
            "pa_decode_shared_prefix", "pa_decode_shared_prefix_workspace_size",
-           "pa_update_key_bounds", "pa_select_blocks")
+           "pa_update_key_bounds", "pa_select_blocks",
+           "pa_decode_selected_blocks_workspace_size", "pa_decode_selected_blocks",
+           "pa_decode_accumulate_weights_workspace_size", "pa_decode_accumulate_weights",
+           "pa_evict_tokens")
 
 
 class PAError(RuntimeError):
@@ -74,6 +77,16 @@ def lib() -> ctypes.CDLL:
         L.pa_decode_shared_prefix_workspace_size.restype = SZ
         L.pa_update_key_bounds.argtypes = [P, P, P, P, P, I, I, I, I, I, I, I, I, P]
         L.pa_select_blocks.argtypes = [P, P, P, P, P, I, I, I, I, I, I, I, I, I, I, I, I, P]
+        L.pa_decode_selected_blocks_workspace_size.argtypes = [I, I, I, I, I, I, I]
+        L.pa_decode_selected_blocks_workspace_size.restype = SZ
+        L.pa_decode_selected_blocks.argtypes = [P, P, P, P, P, P, P, I, I, I, I, I, I, I, I, F,
+                                                I, P, SZ, I, P]
+        L.pa_decode_accumulate_weights_workspace_size.argtypes = [I, I, I, I, I]
+        L.pa_decode_accumulate_weights_workspace_size.restype = SZ
+        L.pa_decode_accumulate_weights.argtypes = [P, P, P, P, P, P, P, P, I, I, I, I, I, I, I,
+                                                   I, I, F, I, P, SZ, I, P]
+        L.pa_evict_tokens.argtypes = [P, P, P, P, P, P, P, P, P, I, I, I, I, I, I, I, I, I, I,
+                                      I, I, I, P]
         L.pa_copy_blocks.argtypes = [P, P, P, I, I, I, I, I, I, P]
         L.pa_swap_blocks.argtypes = [P, P, I, P, P, I, P, I, I, I, I, I, P]
         L.pa_check_tables.argtypes = [P, P, I, I, I, I, P, ctypes.POINTER(I), P]
@@ -87,7 +100,8 @@ def lib() -> ctypes.CDLL:
                   "pa_prefill_chunk_sliding_window", "pa_reshape_and_cache_int8",
                   "pa_decode_int8", "pa_decode_shared_prefix", "pa_device_error",
                   "pa_selftest_bounded_wait", "pa_decode_partition_tokens", "pa_version",
-                  "pa_update_key_bounds", "pa_select_blocks"):
+                  "pa_update_key_bounds", "pa_select_blocks", "pa_decode_selected_blocks",
+                  "pa_decode_accumulate_weights", "pa_evict_tokens"):
             getattr(L, f).restype = I
         _lib = L
     return _lib
@@ -636,3 +650,152 @@ def pa_select_blocks(selected, q, key_bounds, block_tables, context_lens, max_co
     order, -1 past the last."""
     prepare_select_blocks(selected, q, key_bounds, block_tables, context_lens, max_context_len,
                           block_size, num_first, num_last)(stream)
+
+
+def pa_decode_selected_blocks_workspace_size(num_seqs: int, num_q_heads: int, num_kv_heads: int,
+                                             head_dim: int, block_size: int, max_selected: int,
+                                             partition_size: int = 0) -> int:
+    """Bytes of workspace ``pa_decode_selected_blocks`` needs (0: none, or
+    invalid arguments)."""
+    return int(lib().pa_decode_selected_blocks_workspace_size(
+        int(num_seqs), int(num_q_heads), int(num_kv_heads), int(head_dim), int(block_size),
+        int(max_selected), int(partition_size)))
+
+
+def _decode_shapes(out, q, k_cache, v_cache, rows):
+    if q.dim() != 3 or q.shape[0] != rows:
+        raise ValueError("q must be [num_seqs, num_q_heads, head_dim]")
+    if k_cache.dim() != 4 or k_cache.shape != v_cache.shape:
+        raise ValueError("caches must be [num_blocks, num_kv_heads, block_size, head_dim]")
+    if out.shape != q.shape or k_cache.shape[3] != q.shape[2] or out.dtype != q.dtype:
+        raise ValueError("out must match q; caches must share head_dim")
+    if not (q.dtype == k_cache.dtype == v_cache.dtype):
+        raise TypeError("q and caches must share one dtype")
+
+
+def _nbytes(workspace):
+    return 0 if workspace is None else workspace.numel() * workspace.element_size()
+
+
+def prepare_decode_selected_blocks(out, q, k_cache, v_cache, block_tables, context_lens, selected,
+                                   scale: float, partition_size: int = 0,
+                                   workspace: Optional[torch.Tensor] = None) -> Prepared:
+    """``pa_decode_selected_blocks`` with its arguments marshalled once."""
+    _check_int(selected, torch.int32, "selected")
+    B, MB = _rows(block_tables, (context_lens,), ("context_lens",))
+    _decode_shapes(out, q, k_cache, v_cache, B)
+    NB, H_kv, bs, D = k_cache.shape
+    if selected.dim() != 3 or selected.shape[:2] != (B, H_kv):
+        raise ValueError("selected must be [num_seqs, num_kv_heads, max_selected]")
+    return PreparedOn("pa_decode_selected_blocks",
+                      (out, q, k_cache, v_cache, block_tables, context_lens, selected, workspace),
+                      (_p(out), _p(q), _p(k_cache), _p(v_cache), _p(block_tables),
+                       _p(context_lens), _p(selected), selected.shape[2], B, q.shape[1], H_kv, D,
+                       bs, NB, MB, float(scale), int(partition_size), _p(workspace),
+                       _nbytes(workspace), _dt(q)))
+
+
+def pa_decode_selected_blocks(out, q, k_cache, v_cache, block_tables, context_lens, selected,
+                              scale: float, partition_size: int = 0,
+                              workspace: Optional[torch.Tensor] = None, stream=None) -> None:
+    """pa_decode over the blocks ``selected`` [B, H_kv, n] lists for each row
+    and K/V head (places in the row's table; negative entries are padding).
+    ``workspace``: at least :func:`pa_decode_selected_blocks_workspace_size`
+    bytes."""
+    prepare_decode_selected_blocks(out, q, k_cache, v_cache, block_tables, context_lens, selected,
+                                   scale, partition_size, workspace)(stream)
+
+
+def pa_decode_accumulate_weights_workspace_size(num_seqs: int, num_q_heads: int, head_dim: int,
+                                                max_context_len: int,
+                                                partition_size: int = 0) -> int:
+    """Bytes of workspace ``pa_decode_accumulate_weights`` needs (0: none, or
+    invalid arguments)."""
+    return int(lib().pa_decode_accumulate_weights_workspace_size(
+        int(num_seqs), int(num_q_heads), int(head_dim), int(max_context_len),
+        int(partition_size)))
+
+
+def _weights_shape(weights_out, weights_in, rows, heads):
+    """Positions per (row, K/V head) of the weights."""
+    for t, n in ((weights_out, "weights_out"), (weights_in, "weights_in")):
+        if t is None:
+            continue
+        if t.dtype != torch.float32:
+            raise TypeError(f"{n} must be float32")
+        if t.dim() != 3 or t.shape[:2] != (rows, heads) or t.shape != weights_out.shape:
+            raise ValueError(f"{n} must be [num_seqs, num_kv_heads, positions]")
+    return weights_out.shape[2]
+
+
+def prepare_decode_accumulate_weights(out, weights_out, weights_in, q, k_cache, v_cache,
+                                      block_tables, context_lens, max_context_len: int,
+                                      scale: float, partition_size: int = 0,
+                                      workspace: Optional[torch.Tensor] = None) -> Prepared:
+    """``pa_decode_accumulate_weights`` with its arguments marshalled once."""
+    B, MB = _rows(block_tables, (context_lens,), ("context_lens",))
+    _decode_shapes(out, q, k_cache, v_cache, B)
+    NB, H_kv, bs, D = k_cache.shape
+    stride = _weights_shape(weights_out, weights_in, B, H_kv)
+    return PreparedOn("pa_decode_accumulate_weights",
+                      (out, weights_out, weights_in, q, k_cache, v_cache, block_tables,
+                       context_lens, workspace),
+                      (_p(out), _p(weights_out), _p(weights_in), _p(q), _p(k_cache), _p(v_cache),
+                       _p(block_tables), _p(context_lens), B, q.shape[1], H_kv, D, bs, NB, MB,
+                       int(max_context_len), stride, float(scale), int(partition_size),
+                       _p(workspace), _nbytes(workspace), _dt(q)))
+
+
+def pa_decode_accumulate_weights(out, weights_out, weights_in, q, k_cache, v_cache, block_tables,
+                                 context_lens, max_context_len: int, scale: float,
+                                 partition_size: int = 0,
+                                 workspace: Optional[torch.Tensor] = None, stream=None) -> None:
+    """pa_decode that also writes ``weights_out`` [B, H_kv, positions] =
+    ``weights_in`` (None: zeros; may be the same tensor) plus each position's
+    attention weight, added up over the query heads of its K/V head.
+    ``workspace``: at least
+    :func:`pa_decode_accumulate_weights_workspace_size` bytes."""
+    prepare_decode_accumulate_weights(out, weights_out, weights_in, q, k_cache, v_cache,
+                                      block_tables, context_lens, max_context_len, scale,
+                                      partition_size, workspace)(stream)
+
+
+def prepare_evict_tokens(k_cache, v_cache, weights_out, weights_in, kept_positions,
+                         new_context_lens, block_tables, dst_block_tables, context_lens,
+                         max_context_len: int, budget: int, num_first: int = 0,
+                         num_last: int = 0) -> Prepared:
+    """``pa_evict_tokens`` with its arguments marshalled once."""
+    _check_int(kept_positions, torch.int32, "kept_positions")
+    B, MB = _rows(block_tables, (context_lens, new_context_lens),
+                  ("context_lens", "new_context_lens"))
+    dst_rows, dst_MB = _rows(dst_block_tables, (), ())
+    if dst_rows != B:
+        raise ValueError("dst_block_tables must have a row for each of block_tables")
+    if k_cache.dim() != 4 or k_cache.shape != v_cache.shape or k_cache.dtype != v_cache.dtype:
+        raise ValueError("caches must be [num_blocks, num_kv_heads, block_size, head_dim]")
+    NB, H_kv, bs, D = k_cache.shape
+    if weights_in is None:
+        raise ValueError("weights_in is what the tokens are chosen by")
+    stride = _weights_shape(weights_out, weights_in, B, H_kv)
+    if kept_positions.shape != (B, H_kv, int(budget)):
+        raise ValueError("kept_positions must be [num_seqs, num_kv_heads, budget]")
+    return PreparedOn("pa_evict_tokens",
+                      (k_cache, v_cache, weights_out, weights_in, kept_positions,
+                       new_context_lens, block_tables, dst_block_tables, context_lens),
+                      (_p(k_cache), _p(v_cache), _p(weights_out), _p(weights_in),
+                       _p(kept_positions), _p(new_context_lens), _p(block_tables),
+                       _p(dst_block_tables), _p(context_lens), int(budget), int(num_first),
+                       int(num_last), B, H_kv, D, bs, NB, MB, dst_MB, int(max_context_len),
+                       stride, _dt(k_cache)))
+
+
+def pa_evict_tokens(k_cache, v_cache, weights_out, weights_in, kept_positions, new_context_lens,
+                    block_tables, dst_block_tables, context_lens, max_context_len: int,
+                    budget: int, num_first: int = 0, num_last: int = 0, stream=None) -> None:
+    """Keep, for each row and K/V head, the first ``num_first`` and last
+    ``num_last`` positions and those of largest ``weights_in`` between them,
+    ``budget`` in all; move their K, V and weights to the front, in order, into
+    ``dst_block_tables`` (the row's own blocks, or blocks no row reads)."""
+    prepare_evict_tokens(k_cache, v_cache, weights_out, weights_in, kept_positions,
+                         new_context_lens, block_tables, dst_block_tables, context_lens,
+                         max_context_len, budget, num_first, num_last)(stream)

@@ -29,6 +29,7 @@ def clean_error_word(pa):
     pa.pa_device_error(clear=True)
     yield
     torch.cuda.synchronize()
+    pa.pa_device_error(clear=True)
 
 
 def appended(ctxs, hq, hkv, D, bs, dtype, seed, **kw):

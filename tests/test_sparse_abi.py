@@ -61,3 +61,65 @@ def test_select_blocks_host_checks(pa):
         (dict(max_ctx=129), pa.PA_ERR_INVALID_ARG), (dict(max_ctx=-1), pa.PA_ERR_INVALID_ARG),
         (dict(sel=ODD2), pa.PA_ERR_INVALID_ARG), (dict(q=None), pa.PA_ERR_INVALID_ARG),
         (dict(MB=196609, max_ctx=196609 * 16), pa.PA_ERR_UNSUPPORTED)])
+
+
+def test_decode_selected_blocks_host_checks(pa):
+    args = dict(out=FAKE, q=FAKE, k=FAKE, v=FAKE, tables=FAKE, lens=FAKE, sel=FAKE, K=4, B=4,
+                Hq=8, Hkv=2, **SHAPE, scale=0.1, part=0, ws=None, ws_bytes=0, dtype=1)
+    need = pa.pa_decode_selected_blocks_workspace_size(4, 8, 2, 128, 16, 4, 16)
+    o, l_ = 4 * 8 * 4 * 128 * 4, 4 * 8 * 4 * 4
+    assert need == o + l_
+    # one partition needs none; invalid sizes report none
+    f = pa.pa_decode_selected_blocks_workspace_size
+    assert f(4, 8, 2, 128, 16, 4, -1) == 0 and f(4, 8, 2, 128, 16, 0) == 0
+    assert f(4, 7, 2, 128, 16, 4) == 0 and f(4, 8, 2, 128, 16, 4, 24) == 0
+    refusals(pa, "pa_decode_selected_blocks", args, common_cases(pa) + [
+        (dict(Hq=7), pa.PA_ERR_UNSUPPORTED), (dict(K=0), pa.PA_ERR_INVALID_ARG),
+        (dict(scale=float("nan")), pa.PA_ERR_INVALID_ARG), (dict(sel=None), pa.PA_ERR_INVALID_ARG),
+        (dict(sel=ODD2), pa.PA_ERR_INVALID_ARG), (dict(out=ODD4), pa.PA_ERR_INVALID_ARG),
+        (dict(part=24), pa.PA_ERR_INVALID_ARG), (dict(part=32768), pa.PA_ERR_INVALID_ARG),
+        (dict(part=-1, K=1025), pa.PA_ERR_UNSUPPORTED), (dict(K=1 << 28), pa.PA_ERR_UNSUPPORTED),
+        (dict(part=16), pa.PA_ERR_WORKSPACE),
+        (dict(part=16, ws=FAKE, ws_bytes=need - 1), pa.PA_ERR_WORKSPACE),
+        (dict(part=16, ws=ctypes.c_void_p(0x10010), ws_bytes=need), pa.PA_ERR_WORKSPACE)])
+
+
+def test_decode_accumulate_weights_host_checks(pa):
+    args = dict(out=FAKE, wo=FAKE, wi=None, q=FAKE, k=FAKE, v=FAKE, tables=FAKE, lens=FAKE, B=4,
+                Hq=8, Hkv=2, **SHAPE, max_ctx=128, stride=128, scale=0.1, part=0, ws=FAKE,
+                ws_bytes=0, dtype=1)
+    f = pa.pa_decode_accumulate_weights_workspace_size
+    # two statistics per (row, head, partition) and a score per position
+    need = f(4, 8, 128, 128)
+    assert need == 2 * 256 + 4 * 8 * 128 * 4
+    assert f(4, 8, 128, 100, 16) == pa.pa_decode_workspace_size(4, 8, 128, 100, 16) + \
+        2 * 1024 + 4 * 8 * 112 * 4
+    assert f(0, 8, 128, 128) == 0 and f(4, 8, 128, 0) == 0 and f(4, 8, 128, 128, 24) == 0
+    near = ctypes.c_void_p(0x10000 + 64)
+    refusals(pa, "pa_decode_accumulate_weights", args, common_cases(pa) + [
+        (dict(Hq=7), pa.PA_ERR_UNSUPPORTED), (dict(max_ctx=129, stride=256), pa.PA_ERR_INVALID_ARG),
+        (dict(max_ctx=-1), pa.PA_ERR_INVALID_ARG), (dict(stride=127), pa.PA_ERR_INVALID_ARG),
+        (dict(scale=float("inf")), pa.PA_ERR_INVALID_ARG), (dict(wo=None), pa.PA_ERR_INVALID_ARG),
+        (dict(wo=ODD2), pa.PA_ERR_INVALID_ARG), (dict(wi=ODD2), pa.PA_ERR_INVALID_ARG),
+        (dict(wi=near), pa.PA_ERR_INVALID_ARG), (dict(part=24), pa.PA_ERR_INVALID_ARG),
+        (dict(), pa.PA_ERR_WORKSPACE), (dict(ws=None, ws_bytes=need), pa.PA_ERR_WORKSPACE),
+        (dict(ws=ctypes.c_void_p(0x10010), ws_bytes=need), pa.PA_ERR_WORKSPACE)])
+
+
+def test_evict_tokens_host_checks(pa):
+    far = ctypes.c_void_p(0x40000)
+    args = dict(k=FAKE, v=FAKE, wo=FAKE, wi=FAKE, kept=FAKE, new=far, tables=FAKE, dst=FAKE,
+                lens=FAKE, budget=64, first=4, last=8, B=4, Hkv=2, **SHAPE, dst_MB=4, max_ctx=128,
+                stride=128, dtype=1)
+    cases = [c for c in common_cases(pa) if "Hq" not in c[0]]
+    refusals(pa, "pa_evict_tokens", args, cases + [
+        (dict(budget=0), pa.PA_ERR_INVALID_ARG), (dict(first=60, last=5), pa.PA_ERR_INVALID_ARG),
+        (dict(first=-1), pa.PA_ERR_INVALID_ARG),
+        (dict(first=2 ** 31 - 1, last=2 ** 31 - 1), pa.PA_ERR_INVALID_ARG),
+        (dict(dst_MB=0), pa.PA_ERR_INVALID_ARG), (dict(dst_MB=3), pa.PA_ERR_INVALID_ARG),
+        (dict(max_ctx=129, stride=200), pa.PA_ERR_INVALID_ARG),
+        (dict(max_ctx=-1), pa.PA_ERR_INVALID_ARG), (dict(stride=127), pa.PA_ERR_INVALID_ARG),
+        (dict(new=FAKE), pa.PA_ERR_INVALID_ARG), (dict(new=ODD4), pa.PA_ERR_INVALID_ARG),
+        (dict(wi=ctypes.c_void_p(0x10040)), pa.PA_ERR_INVALID_ARG),
+        (dict(wi=None), pa.PA_ERR_INVALID_ARG), (dict(kept=None), pa.PA_ERR_INVALID_ARG),
+        (dict(dst=ODD2), pa.PA_ERR_INVALID_ARG), (dict(k=ODD4), pa.PA_ERR_INVALID_ARG)])
