@@ -249,17 +249,26 @@ pa_status pa_select_blocks(int32_t *selected, const void *q, const void *key_bou
     a.last = num_last;
     int cs = cluster_size((long long)num_seqs * num_kv_heads, blocks, 64);
     while (blocks > (long long)cs * kSelectSegment) cs *= 2;
-    const size_t smem = (size_t)(blocks + cs - 1) / cs * 8 + 8;
+    // keys of a segment and, for the tensor cores, the group's queries beside
+    // them; a segment that leaves no room for those is scored in 64 bits
+    size_t smem = (size_t)(blocks + cs - 1) / cs * 8 + 8;
+    const size_t queries = (size_t)(a.group + 7) / 8 * 8 *
+                           (head_dim == 128 ? kQRow<128> : kQRow<64>);
+    const bool tensor = dtype == PA_BF16 && a.group <= kTensorHeads &&
+                        smem + queries + sizeof(SelectSmem) <= 227 * 1024;
+    if (tensor) smem += queries;
     const dim3 grid((unsigned)cs, (unsigned)num_kv_heads, (unsigned)num_seqs);
-    if (dtype == PA_BF16)
-        return head_dim == 128 ? launch_cluster(select_blocks_kernel<128, __nv_bfloat16>, a, grid,
-                                                kSelThreads, cs, smem, stream)
-                               : launch_cluster(select_blocks_kernel<64, __nv_bfloat16>, a, grid,
-                                                kSelThreads, cs, smem, stream);
-    return head_dim == 128 ? launch_cluster(select_blocks_kernel<128, float>, a, grid, kSelThreads,
-                                            cs, smem, stream)
-                           : launch_cluster(select_blocks_kernel<64, float>, a, grid, kSelThreads,
-                                            cs, smem, stream);
+    auto launch = [&](auto kernel) {
+        return launch_cluster(kernel, a, grid, kSelThreads, cs, smem, stream);
+    };
+    if (dtype == PA_F32)
+        return head_dim == 128 ? launch(select_blocks_kernel<128, float, false>)
+                               : launch(select_blocks_kernel<64, float, false>);
+    if (tensor)
+        return head_dim == 128 ? launch(select_blocks_kernel<128, __nv_bfloat16, true>)
+                               : launch(select_blocks_kernel<64, __nv_bfloat16, true>);
+    return head_dim == 128 ? launch(select_blocks_kernel<128, __nv_bfloat16, false>)
+                           : launch(select_blocks_kernel<64, __nv_bfloat16, false>);
 }
 
 size_t pa_decode_selected_blocks_workspace_size(int num_seqs, int num_q_heads, int num_kv_heads,

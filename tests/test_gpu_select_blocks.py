@@ -219,6 +219,54 @@ def test_scores_that_agree_to_32_bits(pa):
         assert torch.equal(run_select(pa, q, bounds, tables, lens, 1600, 16, 10, 0, 0), want)
 
 
+@pytest.mark.parametrize("near", [2, 30, 256, 257, 1500])
+@pytest.mark.parametrize("batch", [1, 20])
+def test_many_scores_near_the_border(pa, near, batch):
+    """``near`` blocks whose scores differ in the last bits only, with clear
+    winners and clear losers around them and equal ones among them."""
+    n = 2000
+    q, bounds, tables, lens = bounds_case([n * 16] * batch, 8, 2, 128, 16, BF16, 216)
+    g = torch.Generator().manual_seed(217)
+    q.abs_().clamp_(min=0.25)
+    q[:, :, :3] = 1.0
+    bounds[:] = 0.0
+    bounds[:, :, 1, 0] = 2.0 ** 10
+    bounds[:, :, :, 1] = -2.0 ** 10
+    # all blocks far down, then `near` of them at the border, then 20 far up
+    bounds[:, :, 1, 3] = -3.0 - torch.rand(bounds[:, :, 1, 3].shape, generator=g).to(BF16)
+    for b in range(batch):
+        order = tables[b, torch.randperm(n, generator=g)].long()
+        bounds[order[:near], :, 1, 3] = 0.0
+        tiny = torch.randint(0, 1 << 7, (near, 2), generator=g).float() * 2.0 ** -18
+        bounds[order[:near], :, 1, 2] = tiny.to(BF16)
+        bounds[order[near:near + 20], :, 1, 2] = 5.0
+        bounds[order[near:near + 20], :, 1, 3] = 0.0
+    for count in (20 + near // 2, 21, 19 + near):
+        want = R.select_blocks(q, bounds, tables, lens, 16, count, 0, 0)
+        got = run_select(pa, q, bounds, tables, lens, n * 16, 16, count, 0, 0)
+        assert torch.equal(got, want), count
+    assert pa.pa_device_error() == 0
+
+
+@pytest.mark.parametrize("group", [1, 8, 9, 33, 64, 65])
+@pytest.mark.parametrize("D", [64, 128])
+def test_group_sizes(pa, group, D):
+    q, bounds, tables, lens = bounds_case([3000, 1700], 2 * group, 2, D, 16, BF16, 218)
+    want = R.select_blocks(q, bounds, tables, lens, 16, 30, 1, 1)
+    assert torch.equal(run_select(pa, q, bounds, tables, lens, 3000, 16, 30, 1, 1), want)
+
+
+def test_fewer_good_blocks_than_places(pa):
+    """Most of a row's ids are outside the pool: the good ones, then the lowest."""
+    q, bounds, tables, lens = bounds_case([1600], 4, 2, 64, 16, BF16, 219)
+    bad = torch.full_like(tables, -1)
+    good = [90, 7, 33]
+    bad[0, good] = tables[0, good]
+    got = run_select(pa, q, bounds, bad, lens, 1600, 16, 8, 0, 1)
+    assert got[0, 0].tolist() == [0, 1, 2, 3, 7, 33, 90, 99]
+    assert pa.pa_device_error(clear=True) == pa.PA_ERR_BAD_TABLE
+
+
 def test_nan_and_infinite_scores(pa):
     """NaN ranks first, then +inf, ..., then -inf."""
     for dtype in (BF16, F32):
