@@ -411,16 +411,21 @@ PA_API pa_status pa_update_key_bounds(void *key_bounds, const void *k_cache,
  * to the lower index, and a NaN score ranks above every number.
  *   selected     int32 [num_seqs][num_kv_heads][max_selected]
  *   max_selected > 0; num_first + num_last <= max_selected.
- *   max_context_len  host-side upper bound of context_lens, as in pa_decode;
- *                at most 196608 blocks.
+ *   max_context_len  host-side upper bound of context_lens, as in pa_decode.
+ *   workspace    >= pa_select_blocks_workspace_size(...) bytes (8 per row, K/V
+ *                head and block), 256-byte aligned; contents on entry are
+ *                ignored. Calls that may overlap need one each.
  * A block id outside the pool ranks below every score and is recorded as
  * PA_ERR_BAD_TABLE. */
+PA_API size_t pa_select_blocks_workspace_size(int num_seqs, int num_kv_heads, int block_size,
+                                              int max_context_len);
 PA_API pa_status pa_select_blocks(int32_t *selected, const void *q, const void *key_bounds,
                                   const int32_t *block_tables, const int32_t *context_lens,
                                   int max_selected, int num_first, int num_last, int num_seqs,
                                   int num_q_heads, int num_kv_heads, int head_dim,
                                   int block_size, int num_blocks, int max_blocks_per_seq,
-                                  int max_context_len, pa_dtype dtype, cudaStream_t stream);
+                                  int max_context_len, void *workspace, size_t workspace_bytes,
+                                  pa_dtype dtype, cudaStream_t stream);
 
 /* pa_decode over listed blocks only: row b's query heads of K/V head h attend
  * the tokens of the blocks selected[b][h] lists,

@@ -31,6 +31,8 @@
 
 namespace pa {
 
+constexpr int kEvictThreads = 512;
+
 struct EvictArgs {
     char *k_cache, *v_cache;
     float *weights_out;
@@ -56,7 +58,7 @@ __device__ __forceinline__ int evict_len(const EvictArgs &a, int b, bool report)
     return n;
 }
 
-__global__ void __launch_bounds__(kSelThreads)
+__global__ void __launch_bounds__(kEvictThreads)
     evict_select_kernel(const __grid_constant__ EvictArgs a) {
     __shared__ RowSelectSmem sm;
     cg::cluster_group cluster = cg::this_cluster();
@@ -66,7 +68,7 @@ __global__ void __launch_bounds__(kSelThreads)
     const bool lead = rank == 0 && h == 0 && threadIdx.x == 0;
     const int n = evict_len(a, b, lead);
     if (lead) a.new_lens[b] = min(n, a.budget);
-    const int t = rank * kSelThreads + threadIdx.x, threads = ranks * kSelThreads;
+    const int t = rank * kEvictThreads + threadIdx.x, threads = ranks * kEvictThreads;
     if (n <= a.budget) {  // nothing to evict (the whole cluster returns here)
         for (int i = t; i < a.budget; i += threads) dst[i] = i < n ? i : -1;
         return;
@@ -81,8 +83,8 @@ __global__ void __launch_bounds__(kSelThreads)
     const int count = min(seg, middle - s0);
     const float *w = a.weights_in + (size_t)((long long)b * a.H_kv + h) * a.stride + a.first + s0;
     auto key_at = [&](int i) { return order_key(w[i]); };
-    const Cut<uint32_t> cut = cluster_cut<uint32_t>(cluster, sm, key_at, count, (uint32_t)need);
-    cluster_emit<uint32_t>(cluster, sm, key_at, count, cut, [&](int place, int i) {
+    const Cut<uint32_t> cut = cluster_cut<kEvictThreads, uint32_t>(cluster, sm, key_at, count, (uint32_t)need);
+    cluster_emit<kEvictThreads, uint32_t>(cluster, sm, key_at, count, cut, [&](int place, int i) {
         dst[a.first + place] = a.first + s0 + i;
     });
     cluster.sync();  // no CTA exits while another may read its shared memory

@@ -42,7 +42,29 @@ pa_status launch_cluster(K kernel, const A &args, dim3 grid, int threads, int cs
     return launch_status();
 }
 
-constexpr int kSelectSegment = 24576;  // blocks one CTA of a cluster can score
+constexpr int kSelectStage = 24576;  // scores a selecting CTA keeps in shared memory, at most
+
+// A programmatic dependent of the launch before it: its CTAs may be placed
+// while that grid finishes, and wait for it before they use its results.
+template <typename K, typename... A>
+pa_status launch_dependent(K kernel, dim3 grid, int threads, size_t smem, cudaStream_t st,
+                           const A &...args) {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    cfg.stream = st;
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    if (cudaLaunchKernelEx(&cfg, kernel, args...) != cudaSuccess) {
+        cudaGetLastError();
+        return PA_ERR_CUDA;
+    }
+    return launch_status();
+}
 
 // CTAs of a row's cluster: enough for every SM when there are few rows, as
 // long as a CTA keeps `grain` items of the longest row or more.
@@ -207,12 +229,20 @@ pa_status pa_update_key_bounds(void *key_bounds, const void *k_cache, const int3
     return launch_status();
 }
 
+size_t pa_select_blocks_workspace_size(int num_seqs, int num_kv_heads, int block_size,
+                                       int max_context_len) {
+    if (num_seqs <= 0 || num_kv_heads <= 0 || block_size <= 0 || max_context_len <= 0) return 0;
+    return (size_t)num_seqs * num_kv_heads *
+           (((size_t)max_context_len + block_size - 1) / block_size) * sizeof(uint64_t);
+}
+
 pa_status pa_select_blocks(int32_t *selected, const void *q, const void *key_bounds,
                            const int32_t *block_tables, const int32_t *context_lens,
                            int max_selected, int num_first, int num_last, int num_seqs,
                            int num_q_heads, int num_kv_heads, int head_dim, int block_size,
                            int num_blocks, int max_blocks_per_seq, int max_context_len,
-                           pa_dtype dtype, cudaStream_t stream) {
+                           void *workspace, size_t workspace_bytes_given, pa_dtype dtype,
+                           cudaStream_t stream) {
     const pa_status st = check_cache_shape(num_seqs, num_kv_heads, head_dim, block_size,
                                            num_blocks, max_blocks_per_seq, dtype);
     if (st != PA_OK) return st;
@@ -223,7 +253,6 @@ pa_status pa_select_blocks(int32_t *selected, const void *q, const void *key_bou
     if ((long long)max_context_len > (long long)max_blocks_per_seq * block_size)
         return PA_ERR_INVALID_ARG;
     const long long blocks = ((long long)max_context_len + block_size - 1) / block_size;
-    if (blocks > (long long)kMaxCluster * kSelectSegment) return PA_ERR_UNSUPPORTED;
     if (num_seqs == 0) return PA_OK;
     if (!selected || !q || !key_bounds || !block_tables || !context_lens)
         return PA_ERR_INVALID_ARG;
@@ -247,28 +276,63 @@ pa_status pa_select_blocks(int32_t *selected, const void *q, const void *key_bou
     a.K = max_selected;
     a.first = num_first;
     a.last = num_last;
-    int cs = cluster_size((long long)num_seqs * num_kv_heads, blocks, 64);
-    while (blocks > (long long)cs * kSelectSegment) cs *= 2;
-    // keys of a segment and, for the tensor cores, the group's queries beside
-    // them; a segment that leaves no room for those is scored in 64 bits
-    size_t smem = (size_t)(blocks + cs - 1) / cs * 8 + 8;
-    const size_t queries = (size_t)(a.group + 7) / 8 * 8 *
-                           (head_dim == 128 ? kQRow<128> : kQRow<64>);
-    const bool tensor = dtype == PA_BF16 && a.group <= kTensorHeads &&
-                        smem + queries + sizeof(SelectSmem) <= 227 * 1024;
-    if (tensor) smem += queries;
-    const dim3 grid((unsigned)cs, (unsigned)num_kv_heads, (unsigned)num_seqs);
-    auto launch = [&](auto kernel) {
-        return launch_cluster(kernel, a, grid, kSelThreads, cs, smem, stream);
+    a.max_blocks = (int)blocks;
+    a.scores = static_cast<uint64_t *>(workspace);
+    a.stage = (int)std::min<long long>(blocks, kSelectStage);
+    const size_t need =
+        pa_select_blocks_workspace_size(num_seqs, num_kv_heads, block_size, max_context_len);
+    if (need > 0 && (!workspace || workspace_bytes_given < need || !aligned(workspace, 256)))
+        return PA_ERR_WORKSPACE;
+    // longer runs per warp once the grid fills the GPU several times over
+    const long long rows = (long long)num_seqs * num_kv_heads;
+    const int cta_blocks = kScoreWarps * kScoreRows;
+    a.steps = 1;
+    while (a.steps < 4 && rows * blocks > 8LL * 148 * 4 * cta_blocks * a.steps) a.steps *= 2;
+    while (blocks > 65535LL * cta_blocks * a.steps) a.steps *= 2;
+    const long long gy = (blocks + (long long)cta_blocks * a.steps - 1) / (cta_blocks * a.steps);
+    const bool contested = blocks > max_selected && max_selected > num_first + num_last;
+    if (contested) {
+        const dim3 grid((unsigned)num_kv_heads, (unsigned)gy, (unsigned)num_seqs);
+        if (dtype == PA_BF16) {
+            if (head_dim == 128)
+                score_blocks_bf16<128><<<grid, kScoreWarps * 32, 0, stream>>>(a);
+            else
+                score_blocks_bf16<64><<<grid, kScoreWarps * 32, 0, stream>>>(a);
+        } else {
+            if (head_dim == 128)
+                score_blocks_f32<128><<<grid, kScoreWarps * 32, 0, stream>>>(a);
+            else
+                score_blocks_f32<64><<<grid, kScoreWarps * 32, 0, stream>>>(a);
+        }
+        const pa_status scored = launch_status();
+        if (scored != PA_OK) return scored;
+    } else {
+        a.stage = 0;  // no row is scored
+    }
+    auto launch = [&](auto kernel, int threads) {
+        const dim3 grid((unsigned)num_kv_heads, (unsigned)num_seqs);
+        const size_t smem = (size_t)a.stage * sizeof(uint64_t);
+        if (set_smem(kernel, smem) != cudaSuccess) return PA_ERR_CUDA;
+        if (contested) return launch_dependent(kernel, grid, threads, smem, stream, a);
+        // without the scoring kernel in between, the launch before may still
+        // read what this one writes
+        kernel<<<grid, threads, smem, stream>>>(a);
+        return launch_status();
     };
-    if (dtype == PA_F32)
-        return head_dim == 128 ? launch(select_blocks_kernel<128, float, false>)
-                               : launch(select_blocks_kernel<64, float, false>);
-    if (tensor)
-        return head_dim == 128 ? launch(select_blocks_kernel<128, __nv_bfloat16, true>)
-                               : launch(select_blocks_kernel<64, __nv_bfloat16, true>);
-    return head_dim == 128 ? launch(select_blocks_kernel<128, __nv_bfloat16, false>)
-                           : launch(select_blocks_kernel<64, __nv_bfloat16, false>);
+    // many threads for long rows, where a pass over the scores is what counts;
+    // few for short ones, where barriers are
+    if (blocks > 2048) {
+        if (dtype == PA_BF16)
+            return head_dim == 128 ? launch(select_blocks_kernel<1024, 128, __nv_bfloat16>, 1024)
+                                   : launch(select_blocks_kernel<1024, 64, __nv_bfloat16>, 1024);
+        return head_dim == 128 ? launch(select_blocks_kernel<1024, 128, float>, 1024)
+                               : launch(select_blocks_kernel<1024, 64, float>, 1024);
+    }
+    if (dtype == PA_BF16)
+        return head_dim == 128 ? launch(select_blocks_kernel<256, 128, __nv_bfloat16>, 256)
+                               : launch(select_blocks_kernel<256, 64, __nv_bfloat16>, 256);
+    return head_dim == 128 ? launch(select_blocks_kernel<256, 128, float>, 256)
+                           : launch(select_blocks_kernel<256, 64, float>, 256);
 }
 
 size_t pa_decode_selected_blocks_workspace_size(int num_seqs, int num_q_heads, int num_kv_heads,
@@ -395,21 +459,11 @@ pa_status pa_decode_accumulate_weights(void *out, float *weights_out, const floa
     w.vec = weights_stride % 4 == 0 && aligned(weights_out, 16) && aligned(weights_in, 16);
     // programmatic dependent of the split kernel; the merge behind it starts
     // when it has finished
-    cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    cfg.stream = stream;
-    cfg.gridDim = dim3((unsigned)((max_context_len + kWeightTile - 1) / kWeightTile),
-                       (unsigned)num_kv_heads, (unsigned)num_seqs);
-    cfg.blockDim = dim3(kWeightThreads);
-    if (cudaLaunchKernelEx(&cfg, decode_weights_kernel, a, w) != cudaSuccess) {
-        cudaGetLastError();
-        return PA_ERR_CUDA;
-    }
-    if (S <= 1) return launch_status();
+    st = launch_dependent(decode_weights_kernel,
+                          dim3((unsigned)((max_context_len + kWeightTile - 1) / kWeightTile),
+                               (unsigned)num_kv_heads, (unsigned)num_seqs),
+                          kWeightThreads, 0, stream, a, w);
+    if (st != PA_OK || S <= 1) return st;
     if (dtype == PA_BF16)
         return head_dim == 128 ? launch_reduce<128, __nv_bfloat16>(a, stream)
                                : launch_reduce<64, __nv_bfloat16>(a, stream);
@@ -477,7 +531,7 @@ pa_status pa_evict_tokens(void *k_cache, void *v_cache, float *weights_out,
     const int cs = cluster_size(rows, max_context_len, 2048);
     pa_status r = launch_cluster(evict_select_kernel, a,
                                  dim3((unsigned)cs, (unsigned)num_kv_heads, (unsigned)num_seqs),
-                                 kSelThreads, cs, 0, stream);
+                                 kEvictThreads, cs, 0, stream);
     if (r != PA_OK) return r;
     // narrower columns, down to 64 bytes, until there are four CTAs per SM
     a.columns = 1;

@@ -22,9 +22,8 @@ namespace pa {
 
 namespace cg = cooperative_groups;
 
-constexpr int kSelThreads = 512;
-constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kSelItems = 4;      // consecutive items per thread in the scan
+constexpr int kSelMaxWarps = 32;
 constexpr int kMaxCluster = 8;    // portable cluster size
 
 // Unsigned keys in the order of the values; -0 equals +0 and a NaN, of either
@@ -45,7 +44,7 @@ struct RowSelectSmem {
     uint32_t total[256];
     uint32_t digit, above, in_digit;
     uint32_t count[2];                // this CTA's items above the cut, equal to it
-    uint32_t warp_count[kSelWarps];
+    uint32_t warp_count[kSelMaxWarps];
 };
 
 // Items with a key above `key`, and the first `ties` (in order of index) of
@@ -59,7 +58,7 @@ struct Cut {
 // The cut that takes `need` items of the cluster's row; key_at(i), i < n, are
 // this CTA's keys. 1 <= need <= items of the row. Called by every thread of
 // every CTA of the cluster.
-template <typename Key, typename KeyAt>
+template <int THREADS, typename Key, typename KeyAt>
 __device__ __forceinline__ Cut<Key> cluster_cut(cg::cluster_group &cluster, RowSelectSmem &sm,
                                                 const KeyAt &key_at, int n, uint32_t need) {
     const int tid = threadIdx.x;
@@ -71,18 +70,18 @@ __device__ __forceinline__ Cut<Key> cluster_cut(cg::cluster_group &cluster, RowS
         // the other CTAs last read this half two rounds ago, before the
         // cluster barrier of the round in between
         uint32_t *h = sm.hist[round & 1];
-        if (tid < 256) h[tid] = 0;
+        for (int t = tid; t < 256; t += THREADS) h[t] = 0;
         __syncthreads();
-        for (int i = tid; i < n; i += kSelThreads) {
+        for (int i = tid; i < n; i += THREADS) {
             const Key k = key_at(i);
             if (round == 0 || (Key)(k >> shift >> 8) == prefix)
                 atomicAdd(h + ((uint32_t)(k >> shift) & 255u), 1u);
         }
         cluster.sync();
-        if (tid < 256) {
+        for (int t = tid; t < 256; t += THREADS) {
             uint32_t c = 0;
-            for (int r = 0; r < ranks; ++r) c += cluster.map_shared_rank(h, r)[tid];
-            sm.total[tid] = c;
+            for (int r = 0; r < ranks; ++r) c += cluster.map_shared_rank(h, r)[t];
+            sm.total[t] = c;
         }
         __syncthreads();
         if (tid < 32) {  // lane l owns digits 255 - 8l .. 248 - 8l
@@ -120,18 +119,62 @@ __device__ __forceinline__ Cut<Key> cluster_cut(cg::cluster_group &cluster, RowS
     return {prefix, need};
 }
 
+// Sum of `mine` over the threads before this one, and over all in `all`.
+template <int THREADS>
+__device__ __forceinline__ uint32_t block_before(RowSelectSmem &sm, uint32_t mine, uint32_t &all) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    uint32_t upto = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t y = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += y;
+    }
+    if (lane == 31) sm.warp_count[warp] = upto;
+    __syncthreads();
+    uint32_t before = upto - mine;
+    all = 0;
+#pragma unroll
+    for (int w = 0; w < THREADS / 32; ++w) {
+        const uint32_t c = sm.warp_count[w];
+        if (w < warp) before += c;
+        all += c;
+    }
+    __syncthreads();  // before the next use of warp_count
+    return before;
+}
+
+// emit(place, i) for every item i < n of this CTA with taken(i), place
+// ascending with i from `place`.
+template <int THREADS, typename Taken, typename Emit>
+__device__ __forceinline__ void block_emit(RowSelectSmem &sm, int n, uint32_t place,
+                                           const Taken &taken, const Emit &emit) {
+    for (int t0 = 0; t0 < n; t0 += THREADS * kSelItems) {
+        const int i0 = t0 + (int)threadIdx.x * kSelItems;
+        uint32_t in = 0;
+#pragma unroll
+        for (int u = 0; u < kSelItems; ++u)
+            if (i0 + u < n) in |= (uint32_t)taken(i0 + u) << u;
+        uint32_t all;
+        uint32_t at = place + block_before<THREADS>(sm, __popc(in), all);
+#pragma unroll
+        for (int u = 0; u < kSelItems; ++u)
+            if ((in >> u) & 1u) emit((int)at++, i0 + u);
+        place += all;
+    }
+}
+
 // emit(place, i) for every taken item i of this CTA, place ascending with i
 // from the cluster's first item on. Every thread of the cluster calls it; a
 // cluster barrier must follow before a CTA exits or reuses `sm`.
-template <typename Key, typename KeyAt, typename Emit>
+template <int THREADS, typename Key, typename KeyAt, typename Emit>
 __device__ __forceinline__ void cluster_emit(cg::cluster_group &cluster, RowSelectSmem &sm,
                                              const KeyAt &key_at, int n, const Cut<Key> &cut,
                                              const Emit &emit) {
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, lane = tid & 31;
     if (tid < 2) sm.count[tid] = 0;
     __syncthreads();
     uint32_t gt = 0, eq = 0;
-    for (int i = tid; i < n; i += kSelThreads) {
+    for (int i = tid; i < n; i += THREADS) {
         const Key k = key_at(i);
         gt += k > cut.key;
         eq += k == cut.key;
@@ -149,7 +192,7 @@ __device__ __forceinline__ void cluster_emit(cg::cluster_group &cluster, RowSele
         gt_base += c[0];
         eq_base += c[1];
     }
-    for (int t0 = 0; t0 < n; t0 += kSelThreads * kSelItems) {
+    for (int t0 = 0; t0 < n; t0 += THREADS * kSelItems) {
         const int i0 = t0 + tid * kSelItems;
         uint32_t is_gt = 0, is_eq = 0;
 #pragma unroll
@@ -161,23 +204,10 @@ __device__ __forceinline__ void cluster_emit(cg::cluster_group &cluster, RowSele
             }
         }
         // counts before this thread's items: above in the low half, equal in
-        // the high half (a tile has kSelThreads * kSelItems < 65536 items)
+        // the high half (a tile has THREADS * kSelItems < 65536 items)
         const uint32_t mine = __popc(is_gt) | (__popc(is_eq) << 16);
-        uint32_t upto = mine;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const uint32_t y = __shfl_up_sync(0xffffffffu, upto, o);
-            if (lane >= o) upto += y;
-        }
-        if (lane == 31) sm.warp_count[warp] = upto;
-        __syncthreads();
-        uint32_t before = upto - mine, all = 0;
-#pragma unroll
-        for (int w = 0; w < kSelWarps; ++w) {
-            const uint32_t c = sm.warp_count[w];
-            if (w < warp) before += c;
-            all += c;
-        }
+        uint32_t all;
+        const uint32_t before = block_before<THREADS>(sm, mine, all);
         uint32_t g = gt_base + (before & 0xffffu), e = eq_base + (before >> 16);
 #pragma unroll
         for (int u = 0; u < kSelItems; ++u) {
@@ -188,7 +218,6 @@ __device__ __forceinline__ void cluster_emit(cg::cluster_group &cluster, RowSele
         }
         gt_base += all & 0xffffu;
         eq_base += all >> 16;
-        __syncthreads();
     }
 }
 

@@ -14,37 +14,57 @@
 // the sum of 2 D of them is exact in 53 bits unless their exponents span more
 // than 29 bits; rounding can then only reorder blocks whose scores agree to
 // about 2^-45. Computing every score so is bound by the 64-bit sums (0.56 TB/s
-// over 98K blocks of 8 heads; the bounds' bytes would allow 6.5 TB/s), so bf16
-// rows are scored in 32 bits first and only the blocks near the border again:
-//   - the score is a product of the block's 2 D bounds with the vector
+// over 98K blocks of 8 heads, where the bounds' bytes would allow 6.5 TB/s), so
+// every block is scored in 32 bits with an error bound, and only the blocks
+// near the border between in and out are scored again in 64.
+//
+// score_blocks: a warp per 16 blocks of a (row, K/V head).
+//   - bf16: the score is a product of the block's 2 D bounds with the vector
 //     [min(q, 0), max(q, 0)], for all heads of the group: a warp-level
-//     tensor-core product of 16 blocks x 8 heads x 2 D. The bounds go from
-//     global memory straight into the A fragments, 16 bytes a load; a dot
-//     product does not depend on the order of its terms, so the fragments'
-//     k slots take the dimensions in the order those loads bring them. A
-//     second product of the absolute values gives A = sum |terms|;
-//   - its error: a k = 16 step adds 16 exact products to the accumulator, each
-//     of the 17 cut at no less than 2^-23 of the largest, and rounds: at most
+//     tensor-core product of 16 blocks x 8 heads x 2 D. Bounds and queries go
+//     from global memory straight into fragments, 16 bytes a load (8 KB in
+//     flight per warp, no shared memory, no barrier): a dot product does not
+//     depend on the order of its terms, so the k slots take the dimensions in
+//     the order those loads bring them. A second product of the absolute
+//     values gives A = sum |terms|.
+//     Error: a k = 16 step adds 16 exact products to the accumulator, each of
+//     the 17 cut at no less than 2^-23 of the largest, and rounds: at most
 //     18 * 2^-23 A_i for accumulator i's share of A. Four accumulators take
 //     D / 32 steps each (4 at D = 128): 72 * 2^-23 A, plus three additions:
-//     below 2^-16 A. Products that underflow add less than 2^-100;
-//   - with e the largest error bound of the row and t the border of the 32-bit
-//     scores (at least `need` are >= t, fewer are above it, or exactly `need`
-//     are >= t), a block above t + 2e is in and one below t - 2e is out. If
-//     the blocks between are more than the places left, their scores are
-//     computed in 64 bits: a few blocks are then ranked by comparing all pairs,
-//     many (equal blocks, an infinite or NaN score in the row) by a second
-//     selection.
+//     below 2^-16 A. Products that underflow add less than 2^-100.
+//   - fp32: lanes over the dimensions, fused multiply-adds and a shuffle sum:
+//     2 D / 32 + 5 roundings of at most 2^-24 A, below 2^-19 A.
+//   A score and its error bound go to the workspace, 8 bytes per block beside
+//   the 4 D read.
 //
-// One cluster of CTAs per (row, K/V head): each CTA scores a segment of the
-// row's blocks and keeps the keys in shared memory; the cluster then selects
-// (row_select.cuh). One launch, no workspace. Bound by the bounds' bytes:
-// n * 2 * D elements per (row, K/V head).
+// select_blocks: a CTA per (row, K/V head), a programmatic dependent.
+//   - The border is first found to one of 1024 equal bins over the row's range
+//     of 32-bit scores. With e the row's largest error bound, a block whose
+//     score less 2e is in a bin above the border's is in (what scores better in
+//     64 bits lies above that bin too, and that is fewer blocks than there are
+//     places), and one whose score plus 2e is in a bin below it is out. The few
+//     blocks between are scored in 64 bits and ranked by comparing all pairs.
+//   - Where that does not narrow them down (a score far out, equal blocks, an
+//     infinite or NaN score in the row), the border is found exactly by radix
+//     selection (row_select.cuh), and all blocks within 2e of it are scored and
+//     selected in 64 bits.
+//
+// Scoring and selecting in one kernel (a cluster of CTAs per row, scores in
+// shared memory, no workspace) was built first and measured slower: 123 us on
+// 16 rows of 64K to 128K tokens, its CTAs' shares of a row being uneven and the
+// selection's barriers leaving the memory idle.
+// Bound by the bounds' bytes: n * 2 * D elements per (row, K/V head).
 #pragma once
 
+#include "decode.cuh"
 #include "row_select.cuh"
 
 namespace pa {
+
+constexpr int kScoreWarps = 4;
+constexpr int kScoreRows = 16;     // blocks per warp and step
+constexpr int kBins = 1024;
+constexpr int kFewBlocks = 256;    // blocks near the border ranked by pairs
 
 struct SelectArgs {
     int32_t *selected;  // [B][H_kv][K], ascending, -1 past the last
@@ -52,9 +72,35 @@ struct SelectArgs {
     const void *key_bounds;
     const int32_t *block_tables;
     const int32_t *context_lens;
+    uint64_t *scores;   // [B][H_kv][max_blocks]: order key of the score << 32 | error bound
     int H_q, H_kv, group, bs, bs_shift, NB, MB, max_ctx;
-    int K, first, last;
+    int K, first, last, max_blocks;
+    int steps;          // 16-block steps of a scoring warp
+    int stage;          // blocks whose scores fit the selecting CTA's shared memory
 };
+
+// The value of an order key (a NaN for a NaN's).
+__device__ __forceinline__ float key_value(uint32_t k) {
+    return __uint_as_float((k >> 31) ? k & 0x7fffffffu : ~k);
+}
+
+// Blocks of a row, and those between its first and last ones that compete for
+// `need` places (none when every block is taken).
+struct Contest {
+    int n, middle, need;
+};
+__device__ __forceinline__ Contest contest(const SelectArgs &a, int b, bool report) {
+    int ctx = __ldg(a.context_lens + b);
+    if (ctx < 0 || ctx > a.max_ctx) {
+        if (report) flag_error(PA_ERR_BAD_TABLE);
+        ctx = ctx < 0 ? 0 : a.max_ctx;
+    }
+    Contest c;
+    c.n = (int)(((long long)ctx + a.bs - 1) >> a.bs_shift);
+    c.need = a.K - a.first - a.last;
+    c.middle = c.n > a.K && c.need > 0 ? c.n - a.first - a.last : 0;
+    return c;
+}
 
 template <int VEC, typename T>
 __device__ __forceinline__ void load_vec(const T *p, T (&x)[VEC]) {
@@ -68,7 +114,7 @@ __device__ __forceinline__ void load_vec(const T *p, T (&x)[VEC]) {
         *reinterpret_cast<uint32_t *>(x) = __ldg(reinterpret_cast<const uint32_t *>(p));
 }
 
-// Key of a block's score, computed by a whole warp in 64 bits.
+// Order key of a block's score, computed by a whole warp in 64 bits.
 template <int D, typename T>
 __device__ __forceinline__ uint64_t score_key(const SelectArgs &a, const T *q, int id, int h,
                                               int lane) {
@@ -96,277 +142,360 @@ __device__ __forceinline__ uint64_t score_key(const SelectArgs &a, const T *q, i
     return best;
 }
 
-constexpr int kTensorHeads = 64;   // largest group scored on the tensor cores
-constexpr int kFewBlocks = 256;    // blocks near the border ranked by pairs
-
-struct SelectSmem {
-    RowSelectSmem row;
-    uint32_t err;                  // bits of this CTA's largest error bound
-    uint32_t count[2];             // blocks above the border zone, in it
-    uint32_t listed;               // rank 0: blocks in `zone_key`
-    uint64_t zone_key[kFewBlocks];
-    int zone_at[kFewBlocks];
-};
-
-// Bytes of a head's [min(q, 0), max(q, 0)] row: rows 16 banks apart, so that
-// the 8 lanes of a 16-byte load phase (two rows, 64 bytes each) do not meet.
-template <int D>
-constexpr int kQRow = 2 * D * 2 + 64;
-
-// The group's rows, zero past its last head up to a multiple of 8.
-template <int D>
-__device__ __forceinline__ void load_signed_queries(const __nv_bfloat16 *q, int group,
-                                                    uint8_t *dst) {
-    const int rows = (group + 7) / 8 * 8;
-    for (int i = threadIdx.x; i < rows * D; i += kSelThreads) {
-        const int g = i / D, d = i % D;
-        const float x = g < group ? __bfloat162float(q[(size_t)g * D + d]) : 0.f;
-        __nv_bfloat16 *r = reinterpret_cast<__nv_bfloat16 *>(dst + g * kQRow<D>);
-        // a NaN goes into both, as it does into the sum
-        r[d] = __float2bfloat16(x > 0.f ? 0.f : x);
-        r[D + d] = __float2bfloat16(x < 0.f ? 0.f : x);
-    }
+__device__ __forceinline__ uint64_t score_entry(float score, float err) {
+    return (uint64_t)order_key(score) << 32 | __float_as_uint(err);
 }
 
-// Scores of blocks [0, count) of this CTA into the high halves of keys; returns
-// this thread's largest error bound, +inf where a score is not finite.
+template <bool MAX>
+__device__ __forceinline__ uint32_t signed_part(uint32_t q) {
+    const __nv_bfloat162 z = __floats2bfloat162_rn(0.f, 0.f);
+    const __nv_bfloat162 x = *reinterpret_cast<const __nv_bfloat162 *>(&q);
+    const __nv_bfloat162 r = MAX ? __hmax2_nan(x, z) : __hmin2_nan(x, z);  // a NaN stays one
+    return *reinterpret_cast<const uint32_t *>(&r);
+}
+
+// Grid: (K/V head, kScoreWarps * steps * 16 blocks, row).
 template <int D>
-__device__ __forceinline__ float score_segment(const SelectArgs &a, const uint8_t *qs,
-                                               const int32_t *table, int h, int count,
-                                               uint64_t *keys) {
-    constexpr int CH = D / 16;  // 64-byte pieces of a block's 2 D bounds
+__global__ void __launch_bounds__(kScoreWarps * 32, 4)
+    score_blocks_bf16(const __grid_constant__ SelectArgs a) {
+    constexpr int CH = D / 32;  // 64-byte pieces of a row of D
+    allow_dependent_launch();
+    const int h = blockIdx.x, b = blockIdx.z;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int g = lane >> 2, tig = lane & 3;
-    const int tiles = (a.group + 7) / 8;
-    float err = 0.f;
-    for (int i0 = warp * 16; i0 < count; i0 += kSelWarps * 16) {
-        uint4 x[2][CH];
+    const int middle = contest(a, b, false).middle;
+    const int32_t *table = a.block_tables + (size_t)b * a.MB + a.first;
+    uint64_t *out = a.scores + ((size_t)b * a.H_kv + h) * a.max_blocks;
+    const __nv_bfloat16 *q =
+        reinterpret_cast<const __nv_bfloat16 *>(a.q) + ((size_t)b * a.H_q + (size_t)h * a.group) * D;
+
+    int i0 = ((int)blockIdx.y * a.steps * kScoreWarps + warp) * kScoreRows;
+    int ids[2];
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+        const int i = i0 + g + 8 * r;
+        ids[r] = i < middle ? __ldg(table + i) : -1;
+    }
+    for (int step = 0; step < a.steps && i0 < middle; ++step, i0 += kScoreWarps * kScoreRows) {
+        uint4 x[2][2 * CH];
         bool ok[2];
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
-            const int i = i0 + g + 8 * r;
-            const int id = i < count ? __ldg(table + i) : -1;
-            ok[r] = id >= 0 && id < a.NB;
-            if (i < count && !ok[r] && tig == 0) flag_error(PA_ERR_BAD_TABLE);
+            ok[r] = ids[r] >= 0 && ids[r] < a.NB;
+            if (i0 + g + 8 * r < middle && !ok[r] && tig == 0) flag_error(PA_ERR_BAD_TABLE);
             const uint4 *p = reinterpret_cast<const uint4 *>(a.key_bounds) +
-                             ((size_t)(ok[r] ? id : 0) * a.H_kv + h) * (D / 4) + tig;
+                             ((size_t)(ok[r] ? ids[r] : 0) * a.H_kv + h) * (D / 4) + tig;
 #pragma unroll
-            for (int j = 0; j < CH; ++j) x[r][j] = ok[r] ? __ldg(p + 4 * j) : make_uint4(0, 0, 0, 0);
+            for (int j = 0; j < 2 * CH; ++j)
+                x[r][j] = ok[r] ? __ldg(p + 4 * j) : make_uint4(0, 0, 0, 0);
+            // the next step's ids, while these loads are in flight
+            const int i = i0 + kScoreWarps * kScoreRows + g + 8 * r;
+            ids[r] = i < middle && step + 1 < a.steps ? __ldg(table + i) : -1;
         }
         float best[2] = {-INFINITY, -INFINITY}, size[2] = {0.f, 0.f};
-        bool odd[2] = {false, false};  // some head's score is not finite
-        for (int n = 0; n < tiles; ++n) {
-            const uint32_t qr = smem_u32(qs) + (n * 8 + g) * kQRow<D> + tig * 16;
-            float s[4][4] = {}, m[4] = {};
+#pragma unroll 1
+        for (int g0 = 0; g0 < a.group; g0 += 8) {
+            const uint4 *qp = reinterpret_cast<const uint4 *>(q + (size_t)(g0 + g) * D) + tig;
+            const bool live = g0 + g < a.group;
+            uint4 y[CH];
 #pragma unroll
-            for (int j = 0; j < CH; ++j) {
-                uint4 y;  // read again for every tile: registers hold the bounds
-                asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                             : "=r"(y.x), "=r"(y.y), "=r"(y.z), "=r"(y.w)
-                             : "r"(qr + 64 * j));
+            for (int j = 0; j < CH; ++j) y[j] = live ? __ldg(qp + 4 * j) : make_uint4(0, 0, 0, 0);
+            float s[4][4] = {}, m[4] = {};
+            constexpr uint32_t kAbs = 0x7fff7fffu;
+#pragma unroll
+            for (int j = 0; j < 2 * CH; ++j) {
+                const uint4 w = y[j % CH];
+                const uint32_t w0 = j < CH ? signed_part<false>(w.x) : signed_part<true>(w.x);
+                const uint32_t w1 = j < CH ? signed_part<false>(w.y) : signed_part<true>(w.y);
+                const uint32_t w2 = j < CH ? signed_part<false>(w.z) : signed_part<true>(w.z);
+                const uint32_t w3 = j < CH ? signed_part<false>(w.w) : signed_part<true>(w.w);
                 const uint32_t a0[4] = {x[0][j].x, x[1][j].x, x[0][j].y, x[1][j].y};
                 const uint32_t a1[4] = {x[0][j].z, x[1][j].z, x[0][j].w, x[1][j].w};
-                mma_bf16_16816(s[(2 * j) % 4], a0, y.x, y.y);
-                mma_bf16_16816(s[(2 * j + 1) % 4], a1, y.z, y.w);
-                constexpr uint32_t kAbs = 0x7fff7fffu;
+                mma_bf16_16816(s[(2 * j) % 4], a0, w0, w1);
+                mma_bf16_16816(s[(2 * j + 1) % 4], a1, w2, w3);
                 const uint32_t b0[4] = {a0[0] & kAbs, a0[1] & kAbs, a0[2] & kAbs, a0[3] & kAbs};
                 const uint32_t b1[4] = {a1[0] & kAbs, a1[1] & kAbs, a1[2] & kAbs, a1[3] & kAbs};
-                mma_bf16_16816(m, b0, y.x & kAbs, y.y & kAbs);
-                mma_bf16_16816(m, b1, y.z & kAbs, y.w & kAbs);
+                mma_bf16_16816(m, b0, w0 & kAbs, w1 & kAbs);
+                mma_bf16_16816(m, b1, w2 & kAbs, w3 & kAbs);
             }
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                if (n * 8 + 2 * tig + (e & 1) >= a.group) continue;
+                if (g0 + 2 * tig + (e & 1) >= a.group) continue;
                 const float v = (s[0][e] + s[1][e]) + (s[2][e] + s[3][e]);
                 best[e >> 1] = fmaxf(best[e >> 1], v);
-                size[e >> 1] = fmaxf(size[e >> 1], m[e]);
-                odd[e >> 1] |= !(fabsf(v) < INFINITY) || !(m[e] < INFINITY);
+                // no bound on a score that is not finite (m is NaN only if v is)
+                size[e >> 1] = fmaxf(size[e >> 1], fabsf(v) < INFINITY ? m[e] : INFINITY);
             }
         }
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
-            float z = odd[r] ? INFINITY : fmaf(size[r], 0x1p-16f, 0x1p-100f);
+            float e = fmaf(size[r], 0x1p-16f, 0x1p-100f);
 #pragma unroll
             for (int o = 1; o < 4; o <<= 1) {
                 best[r] = fmaxf(best[r], __shfl_xor_sync(0xffffffffu, best[r], o));
-                z = fmaxf(z, __shfl_xor_sync(0xffffffffu, z, o));
+                e = fmaxf(e, __shfl_xor_sync(0xffffffffu, e, o));
             }
             const int i = i0 + g + 8 * r;
-            if (ok[r]) err = fmaxf(err, z);
-            // the lowest key is that of a block outside the pool
-            if (tig == 0 && i < count) keys[i] = ok[r] ? (uint64_t)order_key(best[r]) << 32 : 1ull;
+            // entry 0, below every score: a block outside the pool
+            if (tig == 0 && i < middle) out[i] = ok[r] ? score_entry(best[r], e) : 0;
         }
     }
-    return err;
 }
 
-__device__ __forceinline__ float key_value(uint32_t k) {  // the float of an order_key
-    return __uint_as_float((k >> 31) ? k & 0x7fffffffu : ~k);
+template <int D>
+__global__ void __launch_bounds__(kScoreWarps * 32)
+    score_blocks_f32(const __grid_constant__ SelectArgs a) {
+    constexpr int VEC = D / 32;
+    allow_dependent_launch();
+    const int h = blockIdx.x, b = blockIdx.z;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int middle = contest(a, b, false).middle;
+    const int32_t *table = a.block_tables + (size_t)b * a.MB + a.first;
+    uint64_t *out = a.scores + ((size_t)b * a.H_kv + h) * a.max_blocks;
+    const float *q =
+        reinterpret_cast<const float *>(a.q) + ((size_t)b * a.H_q + (size_t)h * a.group) * D;
+    const int per_cta = kScoreWarps * kScoreRows * a.steps;
+    const int end = min(middle, ((int)blockIdx.y + 1) * per_cta);
+#pragma unroll 2
+    for (int i = (int)blockIdx.y * per_cta + warp; i < end; i += kScoreWarps) {
+        const int id = __ldg(table + i);
+        if (id < 0 || id >= a.NB) {
+            if (lane == 0) {
+                flag_error(PA_ERR_BAD_TABLE);
+                out[i] = 0;
+            }
+            continue;
+        }
+        const float *p = reinterpret_cast<const float *>(a.key_bounds) +
+                         ((size_t)id * a.H_kv + h) * 2 * D + lane * VEC;
+        alignas(16) float lo[VEC], hi[VEC], x[VEC];
+        load_vec<VEC>(p, lo);
+        load_vec<VEC>(p + D, hi);
+        float best = -INFINITY, size = 0.f;
+        for (int g = 0; g < a.group; ++g) {
+            load_vec<VEC>(q + (size_t)g * D + lane * VEC, x);
+            float s = 0.f, m = 0.f;
+#pragma unroll
+            for (int v = 0; v < VEC; ++v) {
+                const float up = x[v] < 0.f ? 0.f : x[v], down = x[v] > 0.f ? 0.f : x[v];
+                s = fmaf(up, hi[v], s);
+                s = fmaf(down, lo[v], s);
+                m = fmaf(fabsf(up), fabsf(hi[v]), m);
+                m = fmaf(fabsf(down), fabsf(lo[v]), m);
+            }
+            s = warp_sum(s);
+            m = warp_sum(m);
+            best = fmaxf(best, s);
+            size = fmaxf(size, fabsf(s) < INFINITY ? m : INFINITY);
+        }
+        if (lane == 0)
+            out[i] = score_entry(best, fmaf(size, 0x1p-19f, 0x1p-100f));
+    }
 }
 
-// The cut of the cluster's row, by 32-bit scores where they decide and 64-bit
-// ones where they do not. keys: order keys of the 32-bit scores in the high
-// halves; on return such that the cut applies to them.
-template <int D, typename T>
-__device__ __forceinline__ Cut<uint64_t> refined_cut(const SelectArgs &a,
-                                                     cg::cluster_group &cluster, SelectSmem &sm,
-                                                     const T *q, const int32_t *table, int h,
-                                                     int s0, int count, uint32_t need,
-                                                     uint64_t *keys) {
+struct SelectSmem {
+    RowSelectSmem row;
+    uint32_t lo, hi, err;     // order keys of the least and largest score, bits of the largest
+                              // error bound
+    uint32_t bins[kBins];
+    int border;               // the bin that holds the border, kBins if there is none
+    uint32_t above, zone;     // blocks above the border zone, in it
+    int zone_at[kFewBlocks];
+    uint64_t zone_key[kFewBlocks];
+};
+
+// 32-bit scores of a row as bins.
+struct Bins {
+    float lo, scale, err;
+    __device__ __forceinline__ int at(float s) const {  // ascending with s
+        return max(0, (int)fminf((s - lo) * scale, (float)(kBins - 1)));
+    }
+};
+
+// Selects and emits where a bin of 32-bit scores narrows the border down;
+// false (for every thread) where it does not, with the keys' high halves as
+// they were.
+template <int THREADS, int D, typename T, typename Emit>
+__device__ __forceinline__ bool select_by_bins(const SelectArgs &a, SelectSmem &sm, const T *q,
+                                               const int32_t *table, int h, int count,
+                                               uint32_t need, uint64_t *keys, const Emit &emit) {
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int ranks = (int)cluster.num_blocks();
-    const Cut<uint32_t> coarse = cluster_cut<uint32_t>(
+    Bins bins;
+    bins.err = __uint_as_float(sm.err);
+    if (sm.lo > sm.hi || !(bins.err < INFINITY)) return false;
+    bins.lo = key_value(sm.lo);
+    const float width = key_value(sm.hi) - bins.lo;
+    bins.scale = width > 0.f ? (float)kBins / width : 0.f;
+    if (!(width < INFINITY) || !(bins.scale < INFINITY)) return false;
+
+    for (int i = tid; i < count; i += THREADS) {
+        const uint32_t k = (uint32_t)(keys[i] >> 32);
+        if (k != 0) atomicAdd(&sm.bins[bins.at(key_value(k))], 1u);
+    }
+    __syncthreads();
+    {  // thread t owns the bins from kBins - 1 - t * PER down
+        constexpr int PER = kBins / THREADS;
+        uint32_t c[PER], mine = 0, all;
+#pragma unroll
+        for (int j = 0; j < PER; ++j) mine += c[j] = sm.bins[kBins - 1 - tid * PER - j];
+        uint32_t above = block_before<THREADS>(sm.row, mine, all);
+#pragma unroll
+        for (int j = 0; j < PER; ++j) {
+            if (above < need && need <= above + c[j]) sm.border = kBins - 1 - tid * PER - j;
+            above += c[j];
+        }
+    }
+    __syncthreads();
+    const int border = sm.border;
+    if (border == kBins) return false;  // fewer blocks inside the pool than places
+
+    // the low half of a key: 2 in, 1 in the zone, 0 out
+    uint32_t above = 0;
+    for (int i = tid; i < count; i += THREADS) {
+        const uint32_t k = (uint32_t)(keys[i] >> 32);
+        uint32_t mark = 0;
+        if (k != 0) {
+            const float s = key_value(k);
+            if (bins.at(__fsub_rd(s, 2.f * bins.err)) > border) {
+                mark = 2;
+                ++above;
+            } else if (bins.at(__fadd_ru(s, 2.f * bins.err)) >= border) {
+                mark = 1;
+                const uint32_t at = atomicAdd(&sm.zone, 1u);
+                if (at < kFewBlocks) sm.zone_at[at] = i;
+            }
+        }
+        keys[i] = (uint64_t)k << 32 | mark;
+    }
+    above = __reduce_add_sync(0xffffffffu, above);
+    if (lane == 0) atomicAdd(&sm.above, above);
+    __syncthreads();
+    const uint32_t zone = sm.zone, places = need - sm.above;
+    uint32_t least = 1;  // the mark of a block that is in
+    if (zone != places) {
+        if (zone > kFewBlocks) return false;
+        least = 2;
+        for (int j = warp; j < (int)zone; j += THREADS / 32) {
+            const uint64_t s = score_key<D, T>(a, q, __ldg(table + sm.zone_at[j]), h, lane);
+            if (lane == 0) sm.zone_key[j] = s;
+        }
+        __syncthreads();
+        // a block of the zone is in when fewer than the places left rank
+        // before it: a larger score, or an equal one at a lower index
+        for (int j = tid; j < (int)zone; j += THREADS) {
+            const uint64_t s = sm.zone_key[j];
+            const int at = sm.zone_at[j];
+            uint32_t before = 0;
+            for (int o = 0; o < (int)zone; ++o) {
+                const uint64_t other = sm.zone_key[o];
+                before += other > s || (other == s && sm.zone_at[o] < at);
+            }
+            if (before < places) keys[at] = 2;
+        }
+        __syncthreads();
+    }
+    block_emit<THREADS>(
+        sm.row, count, 0, [&](int i) { return (uint32_t)keys[i] >= least; }, emit);
+    return true;
+}
+
+// The cut of the row, by 32-bit scores where they decide and 64-bit ones where
+// they do not. keys: order keys of the 32-bit scores in the high halves; on
+// return such that the cut applies to them.
+template <int THREADS, int D, typename T>
+__device__ __noinline__ Cut<uint64_t> exact_cut(const SelectArgs &a, SelectSmem &sm, const T *q,
+                                                const int32_t *table, int h, int count,
+                                                uint32_t need, uint64_t *keys) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    cg::cluster_group cluster = cg::this_cluster();  // of this CTA alone
+    const Cut<uint32_t> coarse = cluster_cut<THREADS, uint32_t>(
         cluster, sm.row, [&](int i) { return (uint32_t)(keys[i] >> 32); }, count, need);
-    // not enough blocks inside the pool: all of them, then the lowest others
-    if (coarse.key == 0) return {1ull, coarse.ties};
-    float e = 0.f;
-    for (int r = 0; r < ranks; ++r)
-        e = fmaxf(e, __uint_as_float(*cluster.map_shared_rank(&sm.err, r)));
-    // order keys of the border zone's ends; the whole row without a bound
+    const float e = __uint_as_float(sm.err);
+    // order keys of the border zone's ends; the whole row without a bound, or
+    // without enough blocks inside the pool
     uint32_t lo = 1, hi = 0xffffffffu;
-    if (e < INFINITY) {
+    if (e < INFINITY && coarse.key != 0) {
         const float t = key_value(coarse.key);
         lo = order_key(__fsub_rd(t, 2.f * e));
         hi = order_key(__fadd_ru(t, 2.f * e));
     }
-    uint32_t above = 0, zone = 0;
-    for (int i = tid; i < count; i += kSelThreads) {
-        const uint32_t k = (uint32_t)(keys[i] >> 32);
-        above += k > hi;
-        zone += k >= lo && k <= hi;
-    }
-    above = __reduce_add_sync(0xffffffffu, above);
-    zone = __reduce_add_sync(0xffffffffu, zone);
-    if (lane == 0) {
-        atomicAdd(&sm.count[0], above);
-        atomicAdd(&sm.count[1], zone);
-    }
-    cluster.sync();
-    above = zone = 0;
-    for (int r = 0; r < ranks; ++r) {
-        const uint32_t *c = cluster.map_shared_rank(sm.count, r);
-        above += c[0];
-        zone += c[1];
-    }
-    if (above + zone == need) return {((uint64_t)lo << 32) - 1, 0};
-
     constexpr uint64_t kIn = ~(uint64_t)0;  // above every score, a NaN's included
-    if (zone <= kFewBlocks) {
-        SelectSmem *lead = cluster.map_shared_rank(&sm, 0);
-        for (int i = warp; i < count; i += kSelWarps) {
-            const uint32_t k = (uint32_t)(keys[i] >> 32);
-            if (k < lo || k > hi) continue;
-            const uint64_t s = score_key<D, T>(a, q, __ldg(table + i), h, lane);
-            if (lane == 0) {
-                const uint32_t at = atomicAdd(&lead->listed, 1u);
-                lead->zone_key[at] = s;
-                lead->zone_at[at] = s0 + i;
-            }
-        }
-        cluster.sync();
-        // a block of the zone is in when fewer than the places left rank
-        // before it: a larger score, or an equal one at a lower index
-        for (int j = warp; j < (int)zone; j += kSelWarps) {
-            const int at = lead->zone_at[j] - s0;
-            if (at < 0 || at >= count) continue;  // another CTA's
-            const uint64_t s = lead->zone_key[j];
-            uint32_t before = 0;
-            for (int o = lane; o < (int)zone; o += 32) {
-                const uint64_t other = lead->zone_key[o];
-                before += other > s || (other == s && lead->zone_at[o] - s0 < at);
-            }
-            before = __reduce_add_sync(0xffffffffu, before);
-            if (lane == 0) keys[at] = before < need - above ? kIn : 0;
-        }
-        __syncthreads();
-        // what is left in the zone's range of keys is out or set above
-        return {hi == 0xffffffffu ? kIn - 1 : ((uint64_t)hi << 32) | 0xffffffffu, 0};
-    }
-    for (int i = warp; i < count; i += kSelWarps) {
+    for (int i = warp; i < count; i += THREADS / 32) {
         const uint32_t k = (uint32_t)(keys[i] >> 32);
-        uint64_t s = k > hi ? kIn : 0;
+        uint64_t s = k > hi ? kIn : k == 0 ? 1 : 0;
+        // what is sure to be out ranks below what is outside the pool; no place
+        // is left for either
         if (k >= lo && k <= hi)
             s = max((uint64_t)2, min(score_key<D, T>(a, q, __ldg(table + i), h, lane), kIn - 1));
-        if (k == 0) s = 1;  // outside the pool
         __syncwarp();
         if (lane == 0) keys[i] = s;
     }
     __syncthreads();
-    return cluster_cut<uint64_t>(
+    return cluster_cut<THREADS, uint64_t>(
         cluster, sm.row, [&](int i) { return keys[i]; }, count, need);
 }
 
-// TENSOR: bf16 and a group of at most kTensorHeads; else every score is
-// computed in 64 bits.
-template <int D, typename T, bool TENSOR>
-__global__ void __launch_bounds__(kSelThreads)
+// Grid: (K/V head, row). A programmatic dependent of the scoring kernel, which
+// began after everything before it had ended: only the scores are waited for.
+template <int THREADS, int D, typename T>
+__global__ void __launch_bounds__(THREADS)
     select_blocks_kernel(const __grid_constant__ SelectArgs a) {
-    extern __shared__ __align__(16) uint8_t select_smem[];
+    extern __shared__ __align__(16) uint64_t staged[];
     __shared__ SelectSmem sm;
-    cg::cluster_group cluster = cg::this_cluster();
-    const int rank = (int)cluster.block_rank(), ranks = (int)cluster.num_blocks();
-    const int h = blockIdx.y, b = blockIdx.z;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int h = blockIdx.x, b = blockIdx.y, tid = threadIdx.x, lane = tid & 31;
     int32_t *dst = a.selected + ((size_t)b * a.H_kv + h) * a.K;
-
-    int ctx = __ldg(a.context_lens + b);
-    if (ctx < 0 || ctx > a.max_ctx) {
-        if (rank == 0 && h == 0 && threadIdx.x == 0) flag_error(PA_ERR_BAD_TABLE);
-        ctx = ctx < 0 ? 0 : a.max_ctx;
-    }
-    const int n = (int)(((long long)ctx + a.bs - 1) >> a.bs_shift);
-    if (n <= a.K) {  // every block is taken (the whole cluster returns here)
-        if (rank == 0)
-            for (int i = threadIdx.x; i < a.K; i += kSelThreads) dst[i] = i < n ? i : -1;
-        return;
-    }
-    if (rank == 0) {
-        for (int i = threadIdx.x; i < a.first; i += kSelThreads) dst[i] = i;
-        for (int i = threadIdx.x; i < a.last; i += kSelThreads)
-            dst[a.K - a.last + i] = n - a.last + i;
-    }
-    const int need = a.K - a.first - a.last;
-    if (need == 0) return;
-    const int middle = n - a.first - a.last;  // more than need
-    const int seg = (middle + ranks - 1) / ranks;
-    const int s0 = min(rank * seg, middle);
-    const int count = min(seg, middle - s0);
-
-    const T *q = reinterpret_cast<const T *>(a.q) + ((size_t)b * a.H_q + (size_t)h * a.group) * D;
-    const int32_t *table = a.block_tables + (size_t)b * a.MB + a.first + s0;
-    Cut<uint64_t> cut;
-    uint64_t *keys;
-    if constexpr (TENSOR) {
-        const int heads = (a.group + 7) / 8 * 8;
-        keys = reinterpret_cast<uint64_t *>(select_smem + heads * kQRow<D>);
-        load_signed_queries<D>(q, a.group, select_smem);
-        if (threadIdx.x == 0) sm.err = sm.listed = sm.count[0] = sm.count[1] = 0;
-        __syncthreads();
-        float err = score_segment<D>(a, select_smem, table, h, count, keys);
-        const uint32_t bits = __reduce_max_sync(0xffffffffu, __float_as_uint(err));  // err >= 0
-        if (lane == 0) atomicMax(&sm.err, bits);
-        __syncthreads();
-        cut = refined_cut<D, T>(a, cluster, sm, q, table, h, s0, count, (uint32_t)need, keys);
+    const Contest c = contest(a, b, h == 0 && tid == 0);
+    if (c.n <= a.K) {  // every block is taken
+        for (int i = tid; i < a.K; i += THREADS) dst[i] = i < c.n ? i : -1;
     } else {
-        keys = reinterpret_cast<uint64_t *>(select_smem);
-        for (int i = warp; i < count; i += kSelWarps) {
-            const int id = __ldg(table + i);
-            uint64_t k = 0;  // a block outside the pool ranks below every score
-            if (id >= 0 && id < a.NB)
-                k = score_key<D, T>(a, q, id, h, lane);
-            else if (lane == 0)
-                flag_error(PA_ERR_BAD_TABLE);
-            if (lane == 0) keys[i] = k;
-        }
-        __syncthreads();
-        cut = cluster_cut<uint64_t>(
-            cluster, sm.row, [&](int i) { return keys[i]; }, count, (uint32_t)need);
+        for (int i = tid; i < a.first; i += THREADS) dst[i] = i;
+        for (int i = tid; i < a.last; i += THREADS) dst[a.K - a.last + i] = c.n - a.last + i;
     }
-    cluster_emit<uint64_t>(
-        cluster, sm.row, [&](int i) { return keys[i]; }, count, cut, [&](int place, int i) {
-            dst[a.first + place] = a.first + s0 + i;
-        });
-    cluster.sync();  // no CTA exits while another may read its shared memory
+    for (int i = tid; i < kBins; i += THREADS) sm.bins[i] = 0;
+    if (tid == 0) {
+        sm.lo = 0xffffffffu;
+        sm.hi = sm.err = sm.above = sm.zone = 0;
+        sm.border = kBins;
+    }
+    wait_for_primary_grid();
+    if (c.middle == 0) return;
+    __syncthreads();
+
+    // the row's scores into shared memory where they fit
+    const int count = c.middle;
+    uint64_t *row = a.scores + ((size_t)b * a.H_kv + h) * a.max_blocks;
+    uint64_t *keys = count <= a.stage ? staged : row;
+    uint32_t lo = 0xffffffffu, hi = 0, err = 0;
+#pragma unroll 4
+    for (int i = tid; i < count; i += THREADS) {
+        const uint64_t x = __ldcg(row + i);
+        const uint32_t k = (uint32_t)(x >> 32);
+        if (k != 0) {
+            lo = min(lo, k);
+            hi = max(hi, k);
+            err = max(err, (uint32_t)x);  // bits of values >= 0 order as the values
+        }
+        if (keys == staged) staged[i] = x;
+    }
+    lo = __reduce_min_sync(0xffffffffu, lo);
+    hi = __reduce_max_sync(0xffffffffu, hi);
+    err = __reduce_max_sync(0xffffffffu, err);
+    if (lane == 0) {
+        atomicMin(&sm.lo, lo);
+        atomicMax(&sm.hi, hi);
+        atomicMax(&sm.err, err);
+    }
+    __syncthreads();
+    const T *q = reinterpret_cast<const T *>(a.q) + ((size_t)b * a.H_q + (size_t)h * a.group) * D;
+    const int32_t *table = a.block_tables + (size_t)b * a.MB + a.first;
+    auto emit = [&](int place, int i) { dst[a.first + place] = a.first + i; };
+    if (!select_by_bins<THREADS, D, T>(a, sm, q, table, h, count, (uint32_t)c.need, keys, emit)) {
+        const Cut<uint64_t> cut =
+            exact_cut<THREADS, D, T>(a, sm, q, table, h, count, (uint32_t)c.need, keys);
+        cg::cluster_group cluster = cg::this_cluster();
+        cluster_emit<THREADS, uint64_t>(
+            cluster, sm.row, [&](int i) { return keys[i]; }, count, cut, emit);
+    }
 }
 
 }  // namespace pa

@@ -29,7 +29,7 @@ EXPORTS = ("pa_reshape_and_cache", "pa_decode_workspace_size", "pa_decode_partit
            "pa_reshape_and_cache_fp8", "pa_decode_fp8", "pa_decode_sliding_window",
            "pa_prefill_chunk_sliding_window", "pa_reshape_and_cache_int8", "pa_decode_int8",
            "pa_decode_shared_prefix", "pa_decode_shared_prefix_workspace_size",
-           "pa_update_key_bounds", "pa_select_blocks",
+           "pa_update_key_bounds", "pa_select_blocks_workspace_size", "pa_select_blocks",
            "pa_decode_selected_blocks_workspace_size", "pa_decode_selected_blocks",
            "pa_decode_accumulate_weights_workspace_size", "pa_decode_accumulate_weights",
            "pa_evict_tokens")
@@ -76,7 +76,9 @@ def lib() -> ctypes.CDLL:
         L.pa_decode_shared_prefix_workspace_size.argtypes = [I, I, I, I, I, I, I, I, I]
         L.pa_decode_shared_prefix_workspace_size.restype = SZ
         L.pa_update_key_bounds.argtypes = [P, P, P, P, P, I, I, I, I, I, I, I, I, P]
-        L.pa_select_blocks.argtypes = [P, P, P, P, P, I, I, I, I, I, I, I, I, I, I, I, I, P]
+        L.pa_select_blocks_workspace_size.argtypes = [I, I, I, I]
+        L.pa_select_blocks_workspace_size.restype = SZ
+        L.pa_select_blocks.argtypes = [P, P, P, P, P, I, I, I, I, I, I, I, I, I, I, I, P, SZ, I, P]
         L.pa_decode_selected_blocks_workspace_size.argtypes = [I, I, I, I, I, I, I]
         L.pa_decode_selected_blocks_workspace_size.restype = SZ
         L.pa_decode_selected_blocks.argtypes = [P, P, P, P, P, P, P, I, I, I, I, I, I, I, I, F,
@@ -560,6 +562,7 @@ class PreparedOn(Prepared):
     def __init__(self, fn: str, tensors, args):
         super().__init__(fn, args)
         self._tensors = [t for t in tensors if t is not None]
+        self.workspace = tensors[-1]  # of the calls that have one
         devices = {t.device for t in self._tensors}
         if len(devices) != 1:
             raise ValueError(f"{fn}: all tensors must be on one device")
@@ -622,10 +625,19 @@ def pa_update_key_bounds(key_bounds, k_cache, block_tables, context_lens, new_le
                               max_new_len)(stream)
 
 
+def pa_select_blocks_workspace_size(num_seqs: int, num_kv_heads: int, block_size: int,
+                                    max_context_len: int) -> int:
+    """Bytes of workspace ``pa_select_blocks`` needs."""
+    return int(lib().pa_select_blocks_workspace_size(int(num_seqs), int(num_kv_heads),
+                                                     int(block_size), int(max_context_len)))
+
+
 def prepare_select_blocks(selected, q, key_bounds, block_tables, context_lens,
                           max_context_len: int, block_size: int, num_first: int = 0,
-                          num_last: int = 0) -> Prepared:
-    """``pa_select_blocks`` with its arguments marshalled once."""
+                          num_last: int = 0,
+                          workspace: Optional[torch.Tensor] = None) -> Prepared:
+    """``pa_select_blocks`` with its arguments marshalled once. Without a
+    ``workspace`` the prepared call gets one of its own."""
     _check_int(selected, torch.int32, "selected")
     B, MB = _rows(block_tables, (context_lens,), ("context_lens",))
     NB, H_kv, D = _bounds_shape(key_bounds)
@@ -635,21 +647,31 @@ def prepare_select_blocks(selected, q, key_bounds, block_tables, context_lens,
         raise ValueError("selected must be [num_seqs, num_kv_heads, max_selected]")
     if q.dtype != key_bounds.dtype:
         raise TypeError("q and key_bounds must share one dtype")
-    return PreparedOn("pa_select_blocks", (selected, q, key_bounds, block_tables, context_lens),
+    if workspace is None:
+        n = pa_select_blocks_workspace_size(B, H_kv, block_size, max_context_len)
+        workspace = torch.empty(n, dtype=torch.uint8, device=q.device)
+    return PreparedOn("pa_select_blocks",
+                      (selected, q, key_bounds, block_tables, context_lens, workspace),
                       (_p(selected), _p(q), _p(key_bounds), _p(block_tables), _p(context_lens),
                        selected.shape[2], int(num_first), int(num_last), B, q.shape[1], H_kv, D,
-                       int(block_size), NB, MB, int(max_context_len), _dt(q)))
+                       int(block_size), NB, MB, int(max_context_len), _p(workspace),
+                       _nbytes(workspace), _dt(q)))
 
 
 def pa_select_blocks(selected, q, key_bounds, block_tables, context_lens, max_context_len: int,
                      block_size: int, num_first: int = 0, num_last: int = 0,
-                     stream=None) -> None:
+                     workspace: Optional[torch.Tensor] = None, stream=None) -> None:
     """List, for each row and K/V head, the ``selected.shape[2]`` blocks whose
     keys' bounds allow the largest products with the row's queries (the first
     ``num_first`` and last ``num_last`` blocks always among them), in ascending
-    order, -1 past the last."""
-    prepare_select_blocks(selected, q, key_bounds, block_tables, context_lens, max_context_len,
-                          block_size, num_first, num_last)(stream)
+    order, -1 past the last. ``workspace``: at least
+    :func:`pa_select_blocks_workspace_size` bytes, allocated for the call when
+    None."""
+    call = prepare_select_blocks(selected, q, key_bounds, block_tables, context_lens,
+                                 max_context_len, block_size, num_first, num_last, workspace)
+    call(stream)
+    if workspace is None and stream is not None:
+        call.workspace.record_stream(stream)
 
 
 def pa_decode_selected_blocks_workspace_size(num_seqs: int, num_q_heads: int, num_kv_heads: int,

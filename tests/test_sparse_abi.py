@@ -52,15 +52,22 @@ def test_update_key_bounds_host_checks(pa):
 
 
 def test_select_blocks_host_checks(pa):
+    need = pa.pa_select_blocks_workspace_size(4, 2, 16, 127)
+    assert need == 4 * 2 * 8 * 8
+    f = pa.pa_select_blocks_workspace_size
+    assert f(0, 2, 16, 128) == 0 and f(4, 2, 16, 0) == 0 and f(4, 0, 16, 128) == 0
+    assert f(65535, 8, 16, 1 << 20) == 65535 * 8 * 65536 * 8
     args = dict(sel=FAKE, q=FAKE, bounds=FAKE, tables=FAKE, lens=FAKE, K=4, first=1, last=1, B=4,
-                Hq=8, Hkv=2, **SHAPE, max_ctx=128, dtype=1)
+                Hq=8, Hkv=2, **SHAPE, max_ctx=128, ws=FAKE, ws_bytes=0, dtype=1)
     refusals(pa, "pa_select_blocks", args, common_cases(pa) + [
         (dict(Hq=7), pa.PA_ERR_UNSUPPORTED), (dict(K=0), pa.PA_ERR_INVALID_ARG),
         (dict(first=-1), pa.PA_ERR_INVALID_ARG), (dict(last=4), pa.PA_ERR_INVALID_ARG),
         (dict(first=2 ** 31 - 1, last=2 ** 31 - 1), pa.PA_ERR_INVALID_ARG),
         (dict(max_ctx=129), pa.PA_ERR_INVALID_ARG), (dict(max_ctx=-1), pa.PA_ERR_INVALID_ARG),
         (dict(sel=ODD2), pa.PA_ERR_INVALID_ARG), (dict(q=None), pa.PA_ERR_INVALID_ARG),
-        (dict(MB=196609, max_ctx=196609 * 16), pa.PA_ERR_UNSUPPORTED)])
+        (dict(), pa.PA_ERR_WORKSPACE), (dict(ws_bytes=need - 1), pa.PA_ERR_WORKSPACE),
+        (dict(ws=None, ws_bytes=need), pa.PA_ERR_WORKSPACE),
+        (dict(ws=ctypes.c_void_p(0x10010), ws_bytes=need), pa.PA_ERR_WORKSPACE)])
 
 
 def test_decode_selected_blocks_host_checks(pa):
