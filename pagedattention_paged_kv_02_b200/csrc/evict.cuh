@@ -9,8 +9,8 @@
 // row's destination table, their weights likewise.
 //
 // Two kernels. evict_select: one cluster of CTAs per (row, K/V head) finds
-// the kept positions (row_select.cuh) straight from the weights in global
-// memory. evict_move: moves the rows.
+// the kept positions (row_select.cuh), the order keys of its weights in shared
+// memory where they fit. evict_move: moves the rows.
 //
 // A destination block may be the row's own block at the same place (the cache
 // is then compacted in place) or a block no row reads. In place, the token
@@ -21,7 +21,10 @@
 // comes before a barrier, every store after it. Tokens of later chunks have
 // positions p_i >= i, which no earlier chunk has written. Columns are
 // independent, which is where the parallelism of a small batch comes from.
-// Tokens that stay where they are are neither read nor written.
+// Tokens that stay where they are are neither read nor written. A row that
+// moves into other blocks throughout has no such order: there a CTA takes a run
+// of whole tokens instead (rows of 256 bytes rather than 64 at a time: 112 us
+// against 90 for 512 MB, four rows of 16K kept tokens).
 //
 // Bound by the bytes: the weights twice, the moved tokens' rows read and
 // written once.
@@ -30,8 +33,6 @@
 #include "row_select.cuh"
 
 namespace pa {
-
-constexpr int kEvictThreads = 512;
 
 struct EvictArgs {
     char *k_cache, *v_cache;
@@ -46,7 +47,8 @@ struct EvictArgs {
     int H_kv, bs, bs_shift, NB, MB, dst_MB, max_ctx;
     int budget, first, last;
     int row_bytes;            // D * element size
-    int columns;              // of K, and of V
+    int parts;                // CTAs that share a (row, K/V head)'s K, and its V
+    int stage;                // weights of a segment that fit shared memory
 };
 
 __device__ __forceinline__ int evict_len(const EvictArgs &a, int b, bool report) {
@@ -58,35 +60,200 @@ __device__ __forceinline__ int evict_len(const EvictArgs &a, int b, bool report)
     return n;
 }
 
-__global__ void __launch_bounds__(kEvictThreads)
+constexpr int kCandidates = 2048;  // of a row, in the bin that holds the border
+
+struct EvictSmem {
+    RowSelectSmem row;
+    uint32_t lo, hi;               // range of this CTA's keys
+    alignas(16) uint32_t bins[kCutBins];
+    uint32_t border, above, in_border;
+    uint32_t candidates;           // of this CTA
+    uint32_t own[kCandidates];     // its candidates
+    uint32_t all[kCandidates];     // the row's
+};
+
+// The cut of the cluster's row with the keys of a CTA's segment in shared
+// memory (0 from n up to a multiple of 8), and the counts cluster_place needs.
+// The time goes into passes over the keys and into meetings of the cluster. So
+// there are three passes, four keys to a read -- one adds the keys to 1024 bins
+// over the row's range, one counts what is above the border's bin and sets aside
+// what is in it, the last one (cluster_place) hands the kept items out -- and
+// every CTA closes in on the border among the row's candidates by itself.
+// False, for the whole cluster, when there are too many candidates.
+template <int T, typename Row>
+__device__ __forceinline__ bool staged_cut(const Row &cluster, EvictSmem &sm, const uint32_t *keys,
+                                           int n, uint32_t need, Cut<uint32_t> &cut) {
+    constexpr int PER = kCutBins / T;
+    const int tid = threadIdx.x, ranks = cluster.ranks();
+    uint32_t lo = 0xffffffffu, hi = 0;
+    for (int r = 0; r < ranks; ++r) {
+        const uint32_t *p = cluster.at(&sm.lo, r);  // lo, hi
+        lo = min(lo, p[0]);
+        hi = max(hi, p[1]);
+    }
+    // the bins cover the 32 octaves below the largest weight, the lowest one all
+    // that is smaller (a zero would stretch them over every exponent)
+    const uint32_t low = hi - min(hi - lo, (1u << 28) - 1);
+    const int shift = max(0, bit_width(hi - low) - 10);
+    auto count_key = [&](uint32_t k) {
+        if (k != 0) atomicAdd(sm.bins + ((max(k, low) - low) >> shift), 1u);
+    };
+    const uint4 *quads = reinterpret_cast<const uint4 *>(keys);
+    const int n_quads = (n + 3) / 4;
+#pragma unroll 2
+    for (int i = tid; i < n_quads; i += T) {
+        const uint4 x = quads[i];
+        count_key(x.x), count_key(x.y), count_key(x.z), count_key(x.w);
+    }
+    cluster.sync();
+    uint32_t c[PER] = {}, mine = 0, all;  // from bin kCutBins - 1 - tid * PER down
+#pragma unroll 8
+    for (int r = 0; r < ranks; ++r) {
+        const uint32_t *p = cluster.at(sm.bins, r) + kCutBins - (tid + 1) * PER;
+        if constexpr (PER == 2) {
+            const uint2 x = *reinterpret_cast<const uint2 *>(p);
+            c[0] += x.y, c[1] += x.x;
+        } else {
+            static_assert(PER == 4, "one wide read");
+            const uint4 x = *reinterpret_cast<const uint4 *>(p);
+            c[0] += x.w, c[1] += x.z, c[2] += x.y, c[3] += x.x;
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < PER; ++j) mine += c[j];
+    uint32_t above = block_before<T>(sm.row, mine, all);
+#pragma unroll
+    for (int j = 0; j < PER; ++j) {
+        if (above < need && need <= above + c[j]) {
+            sm.border = kCutBins - 1 - tid * PER - j;
+            sm.above = above;
+            sm.in_border = c[j];
+        }
+        above += c[j];
+    }
+    __syncthreads();
+    need -= sm.above;
+    // the bin's lowest key (above 0, the padding) and the width of its range
+    const uint32_t first = sm.border == 0 ? lo : low + (sm.border << shift);
+    const uint32_t span = low + (sm.border << shift) + ((1u << shift) - 1) - first;
+    uint32_t gt = 0;
+#pragma unroll 2
+    for (int i = tid; i < n_quads; i += T) {
+        const uint4 q = quads[i];
+        const uint32_t x[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            if (x[u] < first) continue;
+            if (x[u] - first > span) {
+                ++gt;
+            } else {
+                const uint32_t at = atomicAdd(&sm.candidates, 1u);
+                if (at < kCandidates) sm.own[at] = x[u];
+            }
+        }
+    }
+    cluster.sync();
+    const uint32_t inside = sm.candidates;
+    const bool whole = sm.in_border == need;
+    if (whole || span == 0) {  // the bin is taken whole, or is one value
+        cut = whole ? Cut<uint32_t>{first - 1, 0} : Cut<uint32_t>{first, need};
+        add_counts(sm.row, gt, 0);
+        if (tid == 0) atomicAdd(&sm.row.count[whole ? 0 : 1], inside);
+        cluster.sync();
+        return true;
+    }
+    if (sm.in_border > kCandidates) return false;
+    uint32_t rows = 0;
+    for (int r = 0; r < ranks; ++r) {
+        const uint32_t m = *cluster.at(&sm.candidates, r), *p = cluster.at(sm.own, r);
+        for (int i = tid; i < (int)m; i += T) sm.all[rows + i] = p[i];
+        rows += m;
+    }
+    __syncthreads();
+    cut = cluster_cut<T, uint32_t>(
+        OneCta(), sm.row, [&](int i) { return sm.all[i]; }, (int)rows, need);
+    uint32_t eq = 0;
+    for (int i = tid; i < (int)inside; i += T) {
+        gt += sm.own[i] > cut.key;
+        eq += sm.own[i] == cut.key;
+    }
+    add_counts(sm.row, gt, eq);
+    cluster.sync();
+    return true;
+}
+
+template <int T, typename Row>
+__global__ void __launch_bounds__(T)
     evict_select_kernel(const __grid_constant__ EvictArgs a) {
-    __shared__ RowSelectSmem sm;
-    cg::cluster_group cluster = cg::this_cluster();
-    const int rank = (int)cluster.block_rank(), ranks = (int)cluster.num_blocks();
-    const int h = blockIdx.y, b = blockIdx.z;
+    extern __shared__ __align__(16) uint32_t evict_keys[];
+    __shared__ EvictSmem sm;
+    const Row cluster;
+    const int rank = cluster.rank(), ranks = cluster.ranks();
+    const int h = blockIdx.y, b = blockIdx.z, tid = threadIdx.x;
     int32_t *dst = a.kept + (size_t)((long long)b * a.H_kv + h) * a.budget;
-    const bool lead = rank == 0 && h == 0 && threadIdx.x == 0;
+    const bool lead = rank == 0 && h == 0 && tid == 0;
     const int n = evict_len(a, b, lead);
     if (lead) a.new_lens[b] = min(n, a.budget);
-    const int t = rank * kEvictThreads + threadIdx.x, threads = ranks * kEvictThreads;
+    const int t = rank * T + tid, threads = ranks * T;
     if (n <= a.budget) {  // nothing to evict (the whole cluster returns here)
         for (int i = t; i < a.budget; i += threads) dst[i] = i < n ? i : -1;
         return;
     }
     for (int i = t; i < a.first; i += threads) dst[i] = i;
     for (int i = t; i < a.last; i += threads) dst[a.budget - a.last + i] = n - a.last + i;
-    const int need = a.budget - a.first - a.last;
+    const uint32_t need = (uint32_t)(a.budget - a.first - a.last);
     if (need == 0) return;
     const int middle = n - a.first - a.last;  // more than need
     const int seg = (middle + ranks - 1) / ranks;
     const int s0 = min(rank * seg, middle);
     const int count = min(seg, middle - s0);
     const float *w = a.weights_in + (size_t)((long long)b * a.H_kv + h) * a.stride + a.first + s0;
-    auto key_at = [&](int i) { return order_key(w[i]); };
-    const Cut<uint32_t> cut = cluster_cut<kEvictThreads, uint32_t>(cluster, sm, key_at, count, (uint32_t)need);
-    cluster_emit<kEvictThreads, uint32_t>(cluster, sm, key_at, count, cut, [&](int place, int i) {
-        dst[a.first + place] = a.first + s0 + i;
-    });
+    auto emit = [&](int place, int i) { dst[a.first + place] = a.first + s0 + i; };
+    const bool staged = seg <= a.stage;
+    Cut<uint32_t> cut;
+    bool done = false;
+    if (staged) {
+        for (int i = tid; i < kCutBins; i += T) sm.bins[i] = 0;
+        if (tid == 0) {
+            sm.lo = 0xffffffffu;
+            sm.hi = sm.candidates = sm.row.count[0] = sm.row.count[1] = 0;
+        }
+        __syncthreads();
+        uint32_t lo = 0xffffffffu, hi = 0;
+#pragma unroll 8
+        for (int i = tid; i < count; i += T) {
+            const uint32_t k = order_key(__ldg(w + i));
+            evict_keys[i] = k;
+            lo = min(lo, k);
+            hi = max(hi, k);
+        }
+        if (tid < 8 && count + tid < (count + 7) / 8 * 8) evict_keys[count + tid] = 0;
+        lo = __reduce_min_sync(0xffffffffu, lo);
+        hi = __reduce_max_sync(0xffffffffu, hi);
+        if ((tid & 31) == 0) {
+            atomicMin(&sm.lo, lo);
+            atomicMax(&sm.hi, hi);
+        }
+        cluster.sync();
+        done = staged_cut<T>(cluster, sm, evict_keys, count, need, cut);
+    }
+    if (done) {
+        cluster_place<T, 8>(
+            cluster, sm.row,
+            [&](int i0, uint32_t(&k)[8]) {
+                const uint4 *p = reinterpret_cast<const uint4 *>(evict_keys + i0);
+                const uint4 none = make_uint4(0, 0, 0, 0);
+                const uint4 x = i0 < count ? p[0] : none, y = i0 < count ? p[1] : none;
+                k[0] = x.x, k[1] = x.y, k[2] = x.z, k[3] = x.w;
+                k[4] = y.x, k[5] = y.y, k[6] = y.z, k[7] = y.w;
+            },
+            count, cut, emit);
+    } else {  // a long segment, or many nearly equal weights
+        auto key_at = [&](int i) { return staged ? evict_keys[i] : order_key(__ldg(w + i)); };
+        cluster.sync();
+        cut = cluster_cut<T, uint32_t>(cluster, sm.row, key_at, count, need);
+        cluster_emit<T, uint32_t>(cluster, sm.row, key_at, count, cut, emit);
+    }
     cluster.sync();  // no CTA exits while another may read its shared memory
 }
 
@@ -102,18 +269,18 @@ __device__ __forceinline__ uint4 load_row(const char *p) {
     return x;
 }
 
-// Grid: (columns of K, columns of V, weights; K/V head; row).
+// Grid: (parts of K, parts of V, weights; K/V head; row).
 __global__ void __launch_bounds__(kMoveThreads)
     evict_move_kernel(const __grid_constant__ EvictArgs a) {
     constexpr int U = kMoveLoads;
-    constexpr int kMaxChunk = kMoveThreads / 4 * U;  // columns are at least 64 bytes wide
+    constexpr int kMaxChunk = kMoveThreads / 4 * U;  // a token's part has 64 bytes or more
     __shared__ long long from[2][kMaxChunk], to[2][kMaxChunk];
     const int h = blockIdx.y, b = blockIdx.z;
     const int n = evict_len(a, b, false);
     const int kept = min(n, a.budget);
     const int32_t *pos = a.kept + (size_t)((long long)b * a.H_kv + h) * a.budget;
 
-    if ((int)blockIdx.x == 2 * a.columns) {  // the weights' column
+    if ((int)blockIdx.x == 2 * a.parts) {  // the weights
         const size_t row = (size_t)((long long)b * a.H_kv + h) * a.stride;
         const float *in = a.weights_in + row;
         float *out = a.weights_out + row;
@@ -135,22 +302,28 @@ __global__ void __launch_bounds__(kMoveThreads)
         return;
     }
 
-    const bool is_v = (int)blockIdx.x >= a.columns;
-    const int width = a.row_bytes / a.columns;
-    const int per_row = width >> 4;                // threads on one token, a power of two
-    const int chunk = kMoveThreads / per_row * U;  // tokens
-    const int r0 = threadIdx.x / per_row;
-    const int rows = kMoveThreads / per_row;
-    char *cache = (is_v ? a.v_cache : a.k_cache) +
-                  (size_t)((int)blockIdx.x - (is_v ? a.columns : 0)) * width +
-                  (size_t)(threadIdx.x % per_row) * 16;
     const int32_t *src_row = a.block_tables + (size_t)b * a.MB;
     const int32_t *dst_row = a.dst_tables + (size_t)b * a.dst_MB;
+    const bool is_v = (int)blockIdx.x >= a.parts;
+    const int part = (int)blockIdx.x - (is_v ? a.parts : 0);
+    bool stays = false;  // some block is its own destination
+    for (int i = threadIdx.x; i < (kept + a.bs - 1) >> a.bs_shift; i += kMoveThreads)
+        stays |= __ldg(src_row + i) == __ldg(dst_row + i);
+    const bool columns = __syncthreads_or(stays) != 0;
+    const int width = columns ? a.row_bytes / a.parts : a.row_bytes;
+    const int per_row = width >> 4;                // threads on one token, a power of two
+    const int rows = kMoveThreads / per_row;
+    const int chunk = rows * U;                    // tokens
+    const int r0 = threadIdx.x / per_row;
+    const int run = columns ? kept : (kept + a.parts - 1) / a.parts;
+    const int begin = columns ? 0 : min(part * run, kept), end = min(begin + run, kept);
+    char *cache = (is_v ? a.v_cache : a.k_cache) + (columns ? (size_t)part * width : 0) +
+                  (size_t)(threadIdx.x % per_row) * 16;
     // cache rows the chunk's tokens come from and go to, -1 for one that stays
     auto locate = [&](int c0, int half) {
         for (int i = threadIdx.x; i < chunk; i += kMoveThreads) {
             long long s = -1, d = -1;
-            if (c0 + i < kept) {
+            if (c0 + i < end) {
                 const int p = pos[c0 + i], q = c0 + i;
                 const int sb = __ldg(src_row + (p >> a.bs_shift));
                 const int db = __ldg(dst_row + (q >> a.bs_shift));
@@ -165,12 +338,9 @@ __global__ void __launch_bounds__(kMoveThreads)
             to[half][i] = d;
         }
     };
-    locate(0, 0);
-    __syncthreads();
-    int half = 0;
-    for (int c0 = 0; c0 < kept; c0 += chunk, half ^= 1) {
-        uint4 x[U];
-        long long d[U];
+    uint4 x0[U], x1[U];
+    long long d0[U], d1[U];
+    auto load = [&](uint4(&x)[U], long long(&d)[U], int half) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int i = u * rows + r0;
@@ -178,11 +348,26 @@ __global__ void __launch_bounds__(kMoveThreads)
             d[u] = to[half][i];
             if (s >= 0) x[u] = load_row(cache + s * a.row_bytes);
         }
-        locate(c0 + chunk, half ^ 1);
-        __syncthreads();  // every load of the chunk before any of its stores
+    };
+    auto store = [&](const uint4(&x)[U], const long long(&d)[U]) {
 #pragma unroll
         for (int u = 0; u < U; ++u)
             if (d[u] >= 0) *reinterpret_cast<uint4 *>(cache + d[u] * a.row_bytes) = x[u];
+    };
+    if (begin >= end) return;
+    locate(begin, 0);
+    __syncthreads();
+    load(x0, d0, 0);
+    locate(begin + chunk, 1);
+    for (int c0 = begin; c0 < end; c0 += 2 * chunk) {
+        __syncthreads();  // every load of chunk c0 before any of its stores
+        load(x1, d1, 1);
+        locate(c0 + 2 * chunk, 0);
+        store(x0, d0);
+        __syncthreads();  // the same for the chunk behind it
+        load(x0, d0, 0);
+        locate(c0 + 3 * chunk, 1);
+        store(x1, d1);
     }
 }
 

@@ -44,6 +44,8 @@ pa_status launch_cluster(K kernel, const A &args, dim3 grid, int threads, int cs
 
 constexpr int kSelectStage = 24576;  // scores a selecting CTA keeps in shared memory, at most
 
+constexpr int kEvictStage = 40960;   // weights a selecting CTA keeps in shared memory, at most
+
 // A programmatic dependent of the launch before it: its CTAs may be placed
 // while that grid finishes, and wait for it before they use its results.
 template <typename K, typename... A>
@@ -528,15 +530,28 @@ pa_status pa_evict_tokens(void *k_cache, void *v_cache, float *weights_out,
     a.last = num_last;
     a.row_bytes = head_dim * (dtype == PA_BF16 ? 2 : 4);
     const long long rows = (long long)num_seqs * num_kv_heads;
-    const int cs = cluster_size(rows, max_context_len, 2048);
-    pa_status r = launch_cluster(evict_select_kernel, a,
-                                 dim3((unsigned)cs, (unsigned)num_kv_heads, (unsigned)num_seqs),
-                                 kEvictThreads, cs, 0, stream);
+    const int cs = cluster_size(rows, max_context_len, 4096);
+    a.stage = std::min((max_context_len + cs - 1) / cs, kEvictStage);
+    const dim3 grid((unsigned)cs, (unsigned)num_kv_heads, (unsigned)num_seqs);
+    const size_t smem = ((size_t)a.stage + 8) * 4;
+    // a row to a CTA of its own where there are rows enough, or they are short
+    pa_status r = PA_OK;
+    if (cs > 1) {
+        r = launch_cluster(evict_select_kernel<512, CtaCluster>, a, grid, 512, cs, smem, stream);
+    } else if (max_context_len > 16384) {
+        if (set_smem(evict_select_kernel<512, OneCta>, smem) != cudaSuccess) return PA_ERR_CUDA;
+        evict_select_kernel<512, OneCta><<<grid, 512, smem, stream>>>(a);
+        r = launch_status();
+    } else {
+        if (set_smem(evict_select_kernel<256, OneCta>, smem) != cudaSuccess) return PA_ERR_CUDA;
+        evict_select_kernel<256, OneCta><<<grid, 256, smem, stream>>>(a);
+        r = launch_status();
+    }
     if (r != PA_OK) return r;
-    // narrower columns, down to 64 bytes, until there are four CTAs per SM
-    a.columns = 1;
-    while (a.row_bytes / a.columns > 64 && 2 * rows * a.columns < 4 * 148) a.columns *= 2;
-    evict_move_kernel<<<dim3((unsigned)(2 * a.columns + 1), (unsigned)num_kv_heads,
+    // more parts, down to columns of 64 bytes, until there are four CTAs per SM
+    a.parts = 1;
+    while (a.row_bytes / a.parts > 64 && 2 * rows * a.parts < 4 * 148) a.parts *= 2;
+    evict_move_kernel<<<dim3((unsigned)(2 * a.parts + 1), (unsigned)num_kv_heads,
                              (unsigned)num_seqs),
                         kMoveThreads, 0, stream>>>(a);
     return launch_status();

@@ -45,8 +45,8 @@
 //     places), and one whose score plus 2e is in a bin below it is out. The few
 //     blocks between are scored in 64 bits and ranked by comparing all pairs.
 //   - Where that does not narrow them down (a score far out, equal blocks, an
-//     infinite or NaN score in the row), the border is found exactly by radix
-//     selection (row_select.cuh), and all blocks within 2e of it are scored and
+//     infinite or NaN score in the row), the border is found exactly
+//     (row_select.cuh), and all blocks within 2e of it are scored and
 //     selected in 64 bits.
 //
 // Scoring and selecting in one kernel (a cluster of CTAs per row, scores in
@@ -63,7 +63,7 @@ namespace pa {
 
 constexpr int kScoreWarps = 4;
 constexpr int kScoreRows = 16;     // blocks per warp and step
-constexpr int kBins = 1024;
+constexpr int kBins = kCutBins;
 constexpr int kFewBlocks = 256;    // blocks near the border ranked by pairs
 
 struct SelectArgs {
@@ -297,7 +297,6 @@ struct SelectSmem {
     RowSelectSmem row;
     uint32_t lo, hi, err;     // order keys of the least and largest score, bits of the largest
                               // error bound
-    uint32_t bins[kBins];
     int border;               // the bin that holds the border, kBins if there is none
     uint32_t above, zone;     // blocks above the border zone, in it
     int zone_at[kFewBlocks];
@@ -330,14 +329,14 @@ __device__ __forceinline__ bool select_by_bins(const SelectArgs &a, SelectSmem &
 
     for (int i = tid; i < count; i += THREADS) {
         const uint32_t k = (uint32_t)(keys[i] >> 32);
-        if (k != 0) atomicAdd(&sm.bins[bins.at(key_value(k))], 1u);
+        if (k != 0) atomicAdd(&sm.row.bins[0][bins.at(key_value(k))], 1u);
     }
     __syncthreads();
     {  // thread t owns the bins from kBins - 1 - t * PER down
         constexpr int PER = kBins / THREADS;
         uint32_t c[PER], mine = 0, all;
 #pragma unroll
-        for (int j = 0; j < PER; ++j) mine += c[j] = sm.bins[kBins - 1 - tid * PER - j];
+        for (int j = 0; j < PER; ++j) mine += c[j] = sm.row.bins[0][kBins - 1 - tid * PER - j];
         uint32_t above = block_before<THREADS>(sm.row, mine, all);
 #pragma unroll
         for (int j = 0; j < PER; ++j) {
@@ -407,7 +406,7 @@ __device__ __noinline__ Cut<uint64_t> exact_cut(const SelectArgs &a, SelectSmem 
                                                 const int32_t *table, int h, int count,
                                                 uint32_t need, uint64_t *keys) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    cg::cluster_group cluster = cg::this_cluster();  // of this CTA alone
+    const OneCta cluster;
     const Cut<uint32_t> coarse = cluster_cut<THREADS, uint32_t>(
         cluster, sm.row, [&](int i) { return (uint32_t)(keys[i] >> 32); }, count, need);
     const float e = __uint_as_float(sm.err);
@@ -430,7 +429,7 @@ __device__ __noinline__ Cut<uint64_t> exact_cut(const SelectArgs &a, SelectSmem 
         __syncwarp();
         if (lane == 0) keys[i] = s;
     }
-    __syncthreads();
+    cluster.sync();
     return cluster_cut<THREADS, uint64_t>(
         cluster, sm.row, [&](int i) { return keys[i]; }, count, need);
 }
@@ -451,7 +450,7 @@ __global__ void __launch_bounds__(THREADS)
         for (int i = tid; i < a.first; i += THREADS) dst[i] = i;
         for (int i = tid; i < a.last; i += THREADS) dst[a.K - a.last + i] = c.n - a.last + i;
     }
-    for (int i = tid; i < kBins; i += THREADS) sm.bins[i] = 0;
+    for (int i = tid; i < kBins; i += THREADS) sm.row.bins[0][i] = 0;
     if (tid == 0) {
         sm.lo = 0xffffffffu;
         sm.hi = sm.err = sm.above = sm.zone = 0;
@@ -492,7 +491,7 @@ __global__ void __launch_bounds__(THREADS)
     if (!select_by_bins<THREADS, D, T>(a, sm, q, table, h, count, (uint32_t)c.need, keys, emit)) {
         const Cut<uint64_t> cut =
             exact_cut<THREADS, D, T>(a, sm, q, table, h, count, (uint32_t)c.need, keys);
-        cg::cluster_group cluster = cg::this_cluster();
+        const OneCta cluster;
         cluster_emit<THREADS, uint64_t>(
             cluster, sm.row, [&](int i) { return keys[i]; }, count, cut, emit);
     }

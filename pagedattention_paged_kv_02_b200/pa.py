@@ -570,14 +570,17 @@ class PreparedOn(Prepared):
 
     def __call__(self, stream=None):
         if stream is None:
-            stream = torch.cuda.current_stream(self._device)
+            # the stream's handle without a Stream object around it: 0.1 us, not 1.2
+            handle = torch._C._cuda_getCurrentRawStream(self._device)
         elif stream.device_index != self._device:
             raise ValueError(f"{self.name}: the stream is on another device than the tensors")
+        else:
+            handle = stream.cuda_stream
         if torch.cuda.current_device() == self._device:
-            st = self._fn(*self._args, stream.cuda_stream)
+            st = self._fn(*self._args, handle)
         else:
             with torch.cuda.device(self._device):
-                st = self._fn(*self._args, stream.cuda_stream)
+                st = self._fn(*self._args, handle)
         if st != PA_OK:
             raise PAError(self.name, st)
 
