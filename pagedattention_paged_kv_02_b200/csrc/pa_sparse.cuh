@@ -285,16 +285,18 @@ pa_status pa_select_blocks(int32_t *selected, const void *q, const void *key_bou
         pa_select_blocks_workspace_size(num_seqs, num_kv_heads, block_size, max_context_len);
     if (need > 0 && (!workspace || workspace_bytes_given < need || !aligned(workspace, 256)))
         return PA_ERR_WORKSPACE;
-    // longer runs per warp once the grid fills the GPU several times over
-    const long long rows = (long long)num_seqs * num_kv_heads;
-    const int cta_blocks = kScoreWarps * kScoreRows;
-    a.steps = 1;
-    while (a.steps < 4 && rows * blocks > 8LL * 148 * 4 * cta_blocks * a.steps) a.steps *= 2;
-    while (blocks > 65535LL * cta_blocks * a.steps) a.steps *= 2;
-    const long long gy = (blocks + (long long)cta_blocks * a.steps - 1) / (cta_blocks * a.steps);
+    // several tiles to a warp once the grid fills the GPU several times over
+    const long long all_tiles = (blocks + kScoreRows - 1) / kScoreRows;
+    int steps = 1;
+    while (steps < 4 && (long long)num_seqs * num_kv_heads * all_tiles >
+                            8LL * 148 * 4 * kScoreWarps * steps)
+        steps *= 2;
+    a.tiles = (int)((all_tiles + steps - 1) / steps);
+    const long long gx = ((long long)a.tiles * num_kv_heads + kScoreWarps - 1) / kScoreWarps;
+    if (gx > 0x7fffffffLL) return PA_ERR_UNSUPPORTED;
     const bool contested = blocks > max_selected && max_selected > num_first + num_last;
     if (contested) {
-        const dim3 grid((unsigned)num_kv_heads, (unsigned)gy, (unsigned)num_seqs);
+        const dim3 grid((unsigned)gx, (unsigned)num_seqs);
         if (dtype == PA_BF16) {
             if (head_dim == 128)
                 score_blocks_bf16<128><<<grid, kScoreWarps * 32, 0, stream>>>(a);

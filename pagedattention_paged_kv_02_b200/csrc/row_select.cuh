@@ -186,22 +186,28 @@ __device__ __forceinline__ Cut<Key> cluster_cut(const Row &cluster, RowSelectSme
 }
 
 // emit(place, i) for every item i < n of this CTA with taken(i), place
-// ascending with i from `place`.
+// ascending with i from 0. A warp owns a run of items, counts and then emits
+// the taken ones by ballots: one barrier.
 template <int THREADS, typename Taken, typename Emit>
-__device__ __forceinline__ void block_emit(RowSelectSmem &sm, int n, uint32_t place,
-                                           const Taken &taken, const Emit &emit) {
-    for (int t0 = 0; t0 < n; t0 += THREADS * kSelItems) {
-        const int i0 = t0 + (int)threadIdx.x * kSelItems;
-        uint32_t in = 0;
-#pragma unroll
-        for (int u = 0; u < kSelItems; ++u)
-            if (i0 + u < n) in |= (uint32_t)taken(i0 + u) << u;
-        uint32_t all;
-        uint32_t at = place + block_before<THREADS>(sm, __popc(in), all);
-#pragma unroll
-        for (int u = 0; u < kSelItems; ++u)
-            if ((in >> u) & 1u) emit((int)at++, i0 + u);
-        place += all;
+__device__ __forceinline__ void block_emit(RowSelectSmem &sm, int n, const Taken &taken,
+                                           const Emit &emit) {
+    constexpr int W = THREADS / 32;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int run = (n + THREADS - 1) / THREADS * 32;
+    const int begin = min(warp * run, n), end = min(begin + run, n);
+    uint32_t mine = 0;
+#pragma unroll 4
+    for (int i = begin + lane; i < end; i += 32) mine += taken(i);
+    mine = __reduce_add_sync(0xffffffffu, mine);
+    if (lane == 0) sm.warp_count[warp] = mine;
+    __syncthreads();
+    uint32_t place = __reduce_add_sync(0xffffffffu,
+                                       lane < W && lane < warp ? sm.warp_count[lane] : 0u);
+    for (int i0 = begin; i0 < end; i0 += 32) {
+        const bool in = i0 + lane < end && taken(i0 + lane);
+        const uint32_t who = __ballot_sync(0xffffffffu, in);
+        if (in) emit((int)(place + __popc(who & ((1u << lane) - 1))), i0 + lane);
+        place += __popc(who);
     }
 }
 

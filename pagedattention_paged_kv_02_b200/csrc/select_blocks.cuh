@@ -43,7 +43,9 @@
 //     score less 2e is in a bin above the border's is in (what scores better in
 //     64 bits lies above that bin too, and that is fewer blocks than there are
 //     places), and one whose score plus 2e is in a bin below it is out. The few
-//     blocks between are scored in 64 bits and ranked by comparing all pairs.
+//     blocks between are ranked by comparing all pairs, those of them whose
+//     32-bit scores are within 2e of each other at the border by scores in 64
+//     bits.
 //   - Where that does not narrow them down (a score far out, equal blocks, an
 //     infinite or NaN score in the row), the border is found exactly
 //     (row_select.cuh), and all blocks within 2e of it are scored and
@@ -75,7 +77,7 @@ struct SelectArgs {
     uint64_t *scores;   // [B][H_kv][max_blocks]: order key of the score << 32 | error bound
     int H_q, H_kv, group, bs, bs_shift, NB, MB, max_ctx;
     int K, first, last, max_blocks;
-    int steps;          // 16-block steps of a scoring warp
+    int tiles;          // 16-block tiles of a row that are scored at once
     int stage;          // blocks whose scores fit the selecting CTA's shared memory
 };
 
@@ -125,6 +127,7 @@ __device__ __forceinline__ uint64_t score_key(const SelectArgs &a, const T *q, i
     load_vec<VEC>(lo_p, lo);
     load_vec<VEC>(lo_p + D, hi);
     uint64_t best = 0;
+#pragma unroll 4
     for (int g = 0; g < a.group; ++g) {
         load_vec<VEC>(q + (size_t)g * D + lane * VEC, qv);
         double s = 0.0;
@@ -154,29 +157,34 @@ __device__ __forceinline__ uint32_t signed_part(uint32_t q) {
     return *reinterpret_cast<const uint32_t *>(&r);
 }
 
-// Grid: (K/V head, kScoreWarps * steps * 16 blocks, row).
+// Warp w of a row's scoring warps takes 16-block tile w / H_kv of K/V head
+// w % H_kv -- the heads' bounds of a block lie together -- and every
+// `tiles`-th tile behind it. Grid: (the row's warps / kScoreWarps, row).
 template <int D>
 __global__ void __launch_bounds__(kScoreWarps * 32, 4)
     score_blocks_bf16(const __grid_constant__ SelectArgs a) {
     constexpr int CH = D / 32;  // 64-byte pieces of a row of D
     allow_dependent_launch();
-    const int h = blockIdx.x, b = blockIdx.z;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int b = blockIdx.y, lane = threadIdx.x & 31;
     const int g = lane >> 2, tig = lane & 3;
+    const int w = (int)blockIdx.x * kScoreWarps + (threadIdx.x >> 5);
+    const int first_tile = w / a.H_kv, h = w - first_tile * a.H_kv;
+    if (first_tile >= a.tiles) return;
     const int middle = contest(a, b, false).middle;
     const int32_t *table = a.block_tables + (size_t)b * a.MB + a.first;
     uint64_t *out = a.scores + ((size_t)b * a.H_kv + h) * a.max_blocks;
     const __nv_bfloat16 *q =
         reinterpret_cast<const __nv_bfloat16 *>(a.q) + ((size_t)b * a.H_q + (size_t)h * a.group) * D;
 
-    int i0 = ((int)blockIdx.y * a.steps * kScoreWarps + warp) * kScoreRows;
+    const int stride = a.tiles * kScoreRows;
+    int i0 = first_tile * kScoreRows;
     int ids[2];
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
         const int i = i0 + g + 8 * r;
         ids[r] = i < middle ? __ldg(table + i) : -1;
     }
-    for (int step = 0; step < a.steps && i0 < middle; ++step, i0 += kScoreWarps * kScoreRows) {
+    for (; i0 < middle; i0 += stride) {
         uint4 x[2][2 * CH];
         bool ok[2];
 #pragma unroll
@@ -189,8 +197,8 @@ __global__ void __launch_bounds__(kScoreWarps * 32, 4)
             for (int j = 0; j < 2 * CH; ++j)
                 x[r][j] = ok[r] ? __ldg(p + 4 * j) : make_uint4(0, 0, 0, 0);
             // the next step's ids, while these loads are in flight
-            const int i = i0 + kScoreWarps * kScoreRows + g + 8 * r;
-            ids[r] = i < middle && step + 1 < a.steps ? __ldg(table + i) : -1;
+            const long long i = (long long)i0 + stride + g + 8 * r;
+            ids[r] = i < middle ? __ldg(table + i) : -1;
         }
         float best[2] = {-INFINITY, -INFINITY}, size[2] = {0.f, 0.f};
 #pragma unroll 1
@@ -247,49 +255,52 @@ __global__ void __launch_bounds__(kScoreWarps * 32)
     score_blocks_f32(const __grid_constant__ SelectArgs a) {
     constexpr int VEC = D / 32;
     allow_dependent_launch();
-    const int h = blockIdx.x, b = blockIdx.z;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int b = blockIdx.y, lane = threadIdx.x & 31;
+    const int w = (int)blockIdx.x * kScoreWarps + (threadIdx.x >> 5);
+    const int first_tile = w / a.H_kv, h = w - first_tile * a.H_kv;
+    if (first_tile >= a.tiles) return;
     const int middle = contest(a, b, false).middle;
     const int32_t *table = a.block_tables + (size_t)b * a.MB + a.first;
     uint64_t *out = a.scores + ((size_t)b * a.H_kv + h) * a.max_blocks;
     const float *q =
         reinterpret_cast<const float *>(a.q) + ((size_t)b * a.H_q + (size_t)h * a.group) * D;
-    const int per_cta = kScoreWarps * kScoreRows * a.steps;
-    const int end = min(middle, ((int)blockIdx.y + 1) * per_cta);
+    for (int i0 = first_tile * kScoreRows; i0 < middle; i0 += a.tiles * kScoreRows) {
+        const int end = min(middle, i0 + kScoreRows);
 #pragma unroll 2
-    for (int i = (int)blockIdx.y * per_cta + warp; i < end; i += kScoreWarps) {
-        const int id = __ldg(table + i);
-        if (id < 0 || id >= a.NB) {
-            if (lane == 0) {
-                flag_error(PA_ERR_BAD_TABLE);
-                out[i] = 0;
+        for (int i = i0; i < end; ++i) {
+            const int id = __ldg(table + i);
+            if (id < 0 || id >= a.NB) {
+                if (lane == 0) {
+                    flag_error(PA_ERR_BAD_TABLE);
+                    out[i] = 0;
+                }
+                continue;
             }
-            continue;
-        }
-        const float *p = reinterpret_cast<const float *>(a.key_bounds) +
-                         ((size_t)id * a.H_kv + h) * 2 * D + lane * VEC;
-        alignas(16) float lo[VEC], hi[VEC], x[VEC];
-        load_vec<VEC>(p, lo);
-        load_vec<VEC>(p + D, hi);
-        float best = -INFINITY, size = 0.f;
-        for (int g = 0; g < a.group; ++g) {
-            load_vec<VEC>(q + (size_t)g * D + lane * VEC, x);
-            float s = 0.f, m = 0.f;
+            const float *p = reinterpret_cast<const float *>(a.key_bounds) +
+                             ((size_t)id * a.H_kv + h) * 2 * D + lane * VEC;
+            alignas(16) float lo[VEC], hi[VEC], x[VEC];
+            load_vec<VEC>(p, lo);
+            load_vec<VEC>(p + D, hi);
+            float best = -INFINITY, size = 0.f;
+            for (int g = 0; g < a.group; ++g) {
+                load_vec<VEC>(q + (size_t)g * D + lane * VEC, x);
+                float s = 0.f, m = 0.f;
 #pragma unroll
-            for (int v = 0; v < VEC; ++v) {
-                const float up = x[v] < 0.f ? 0.f : x[v], down = x[v] > 0.f ? 0.f : x[v];
-                s = fmaf(up, hi[v], s);
-                s = fmaf(down, lo[v], s);
-                m = fmaf(fabsf(up), fabsf(hi[v]), m);
-                m = fmaf(fabsf(down), fabsf(lo[v]), m);
+                for (int v = 0; v < VEC; ++v) {
+                    const float up = x[v] < 0.f ? 0.f : x[v], down = x[v] > 0.f ? 0.f : x[v];
+                    s = fmaf(up, hi[v], s);
+                    s = fmaf(down, lo[v], s);
+                    m = fmaf(fabsf(up), fabsf(hi[v]), m);
+                    m = fmaf(fabsf(down), fabsf(lo[v]), m);
+                }
+                s = warp_sum(s);
+                m = warp_sum(m);
+                best = fmaxf(best, s);
+                size = fmaxf(size, fabsf(s) < INFINITY ? m : INFINITY);
             }
-            s = warp_sum(s);
-            m = warp_sum(m);
-            best = fmaxf(best, s);
-            size = fmaxf(size, fabsf(s) < INFINITY ? m : INFINITY);
+            if (lane == 0)
+                out[i] = score_entry(best, fmaf(size, 0x1p-19f, 0x1p-100f));
         }
-        if (lane == 0)
-            out[i] = score_entry(best, fmaf(size, 0x1p-19f, 0x1p-100f));
     }
 }
 
@@ -299,8 +310,10 @@ struct SelectSmem {
                               // error bound
     int border;               // the bin that holds the border, kBins if there is none
     uint32_t above, zone;     // blocks above the border zone, in it
+    uint32_t sure, close;     // blocks of the zone that are in, that 32 bits do not decide
     int zone_at[kFewBlocks];
-    uint64_t zone_key[kFewBlocks];
+    int close_at[kFewBlocks];
+    uint64_t close_key[kFewBlocks];
 };
 
 // 32-bit scores of a row as bins.
@@ -374,27 +387,51 @@ __device__ __forceinline__ bool select_by_bins(const SelectArgs &a, SelectSmem &
     if (zone != places) {
         if (zone > kFewBlocks) return false;
         least = 2;
-        for (int j = warp; j < (int)zone; j += THREADS / 32) {
-            const uint64_t s = score_key<D, T>(a, q, __ldg(table + sm.zone_at[j]), h, lane);
-            if (lane == 0) sm.zone_key[j] = s;
+        const uint32_t *high = reinterpret_cast<const uint32_t *>(keys) + 1;
+        for (int j = tid; j < (int)zone; j += THREADS) {
+            const int at = sm.zone_at[j];
+            const float s = key_value(high[2 * at]);
+            const float up = __fadd_ru(s, 2.f * bins.err), down = __fsub_rd(s, 2.f * bins.err);
+            uint32_t better = 0, not_worse = 0;
+            for (int o = 0; o < (int)zone; ++o) {
+                const float other = key_value(high[2 * sm.zone_at[o]]);
+                better += other > up;
+                not_worse += other >= down;
+            }
+            if (not_worse <= places) {
+                *reinterpret_cast<uint32_t *>(keys + at) = 2;  // the low half
+                atomicAdd(&sm.sure, 1u);
+            } else if (better < places) {
+                sm.close_at[atomicAdd(&sm.close, 1u)] = at;
+            }
         }
         __syncthreads();
-        // a block of the zone is in when fewer than the places left rank
-        // before it: a larger score, or an equal one at a lower index
-        for (int j = tid; j < (int)zone; j += THREADS) {
-            const uint64_t s = sm.zone_key[j];
-            const int at = sm.zone_at[j];
-            uint32_t before = 0;
-            for (int o = 0; o < (int)zone; ++o) {
-                const uint64_t other = sm.zone_key[o];
-                before += other > s || (other == s && sm.zone_at[o] < at);
+        const uint32_t close = sm.close, left = places - sm.sure;
+        if (close != left) {
+            for (int j = warp; j < (int)close; j += THREADS / 32) {
+                const uint64_t s = score_key<D, T>(a, q, __ldg(table + sm.close_at[j]), h, lane);
+                if (lane == 0) sm.close_key[j] = s;
             }
-            if (before < places) keys[at] = 2;
+            __syncthreads();
+        }
+        // one of these is in when fewer than the places left rank before it: a
+        // larger score, or an equal one at a lower index
+        for (int j = tid; j < (int)close; j += THREADS) {
+            const int at = sm.close_at[j];
+            uint32_t before = 0;
+            if (close != left) {
+                const uint64_t s = sm.close_key[j];
+                for (int o = 0; o < (int)close; ++o) {
+                    const uint64_t other = sm.close_key[o];
+                    before += other > s || (other == s && sm.close_at[o] < at);
+                }
+            }
+            if (before < left) keys[at] = 2;
         }
         __syncthreads();
     }
     block_emit<THREADS>(
-        sm.row, count, 0, [&](int i) { return (uint32_t)keys[i] >= least; }, emit);
+        sm.row, count, [&](int i) { return (uint32_t)keys[i] >= least; }, emit);
     return true;
 }
 
@@ -453,7 +490,7 @@ __global__ void __launch_bounds__(THREADS)
     for (int i = tid; i < kBins; i += THREADS) sm.row.bins[0][i] = 0;
     if (tid == 0) {
         sm.lo = 0xffffffffu;
-        sm.hi = sm.err = sm.above = sm.zone = 0;
+        sm.hi = sm.err = sm.above = sm.zone = sm.sure = sm.close = 0;
         sm.border = kBins;
     }
     wait_for_primary_grid();
