@@ -68,6 +68,11 @@ struct DecodeArgs {
     // the unrounded weights relative to it, [B][H_q][S_max]
     float *scores, *part_m, *part_l;
     int score_stride;
+    float *weights_out;        // [B][H_kv][weight_stride]
+    const float *weights_in;   // may be null (zeros) or weights_out
+    long long weight_stride;
+    int weight_vec;            // rows of weights allow 16-byte accesses
+    int weights_here;          // one partition and one head tile: no second kernel
 };
 
 // What a split kernel attends to and leaves behind.
@@ -217,11 +222,73 @@ __device__ __forceinline__ void write_zero_rows(const DecodeArgs &a, int b, int 
     }
 }
 
-// kWeighted: the maximum and the sum of weights of a partition's rows.
+// kWeighted: adds the weights of positions t .. t + 3 of `n` query heads, whose
+// scores start at `sc` and whose statistics are top and inv = 1 / U, to sum.
+__device__ __forceinline__ void add_weights(const DecodeArgs &a, const float *sc, int n,
+                                            const float *top, const float *inv, float (&sum)[4]) {
+#pragma unroll 4
+    for (int g = 0; g < n; ++g) {
+        // whole 16-token chunks of scores were written
+        const float4 x = *reinterpret_cast<const float4 *>(sc + (size_t)g * a.score_stride);
+        const float M = top[g], r = inv[g];
+        if (r == 0.f) continue;  // no usable token
+        sum[0] = fmaf(exp2f(x.x - M), r, sum[0]);
+        sum[1] = fmaf(exp2f(x.y - M), r, sum[1]);
+        sum[2] = fmaf(exp2f(x.z - M), r, sum[2]);
+        sum[3] = fmaf(exp2f(x.w - M), r, sum[3]);
+    }
+}
+
+// kWeighted: weights_out = weights_in + sum at positions t .. t + 3 below ctx.
+__device__ __forceinline__ void write_weights(const DecodeArgs &a, int b, int kvh, int t, int ctx,
+                                              float (&sum)[4]) {
+    const size_t at = (size_t)((long long)b * a.H_kv + kvh) * a.weight_stride + t;
+    if (a.weight_vec && t + 4 <= ctx) {
+        if (a.weights_in) {
+            const float4 x = *reinterpret_cast<const float4 *>(a.weights_in + at);
+            sum[0] += x.x, sum[1] += x.y, sum[2] += x.z, sum[3] += x.w;
+        }
+        *reinterpret_cast<float4 *>(a.weights_out + at) =
+            make_float4(sum[0], sum[1], sum[2], sum[3]);
+    } else {
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+            if (t + u < ctx)
+                a.weights_out[at + u] = (a.weights_in ? a.weights_in[at + u] : 0.f) + sum[u];
+    }
+}
+
+// kWeighted: the maximum and the sum of weights of a partition's rows; with
+// weights_here the CTA has every score of its K/V head and finishes the weights.
 template <int NW, int HT>
-__device__ __forceinline__ void write_statistics(const DecodeArgs &a, const float *red_m,
-                                                 const float *red_u, int b, int h0, int nh,
-                                                 int s) {
+__device__ __forceinline__ void write_statistics(const DecodeArgs &a, float *red_m, float *red_u,
+                                                 int b, int h0, int nh, int s, int kvh, int ctx) {
+    if (a.weights_here) {
+        float M = -INFINITY, U = 0.f;
+        if (threadIdx.x < nh) {
+            const int row = threadIdx.x;
+#pragma unroll
+            for (int w = 0; w < NW; ++w) M = fmaxf(M, red_m[w * HT + row]);
+            if (M != -INFINITY) {
+#pragma unroll
+                for (int w = 0; w < NW; ++w)
+                    U += exp2f(red_m[w * HT + row] - M) * red_u[w * HT + row];
+            }
+        }
+        __syncthreads();  // the rows' maxima have been used
+        if (threadIdx.x < nh) {
+            red_m[threadIdx.x] = M;
+            red_u[threadIdx.x] = U == 0.f ? 0.f : 1.f / U;
+        }
+        __syncthreads();
+        const float *sc = a.scores + ((size_t)b * a.H_q + h0) * a.score_stride;
+        for (int t = 4 * threadIdx.x; t < ctx; t += 4 * NW * 32) {
+            float sum[4] = {0.f, 0.f, 0.f, 0.f};
+            add_weights(a, sc + t, nh, red_m, red_u, sum);
+            write_weights(a, b, kvh, t, ctx, sum);
+        }
+        return;
+    }
     for (int row = threadIdx.x; row < nh; row += NW * 32) {
         float M = -INFINITY, U = 0.f;
 #pragma unroll
@@ -623,7 +690,7 @@ __global__ void __launch_bounds__(NW * 32)
     } else {
         decode_epilogue<D, NW, HT, __nv_bfloat16>(a, red_o, red_m, red_l, b, h0, nh, s, n_splits);
         if constexpr (WEIGHTED)
-            write_statistics<NW, HT>(a, red_m, red_l + NW * HT, b, h0, nh, s);
+            write_statistics<NW, HT>(a, red_m, red_l + NW * HT, b, h0, nh, s, kvh, ctx);
     }
 }
 
@@ -816,7 +883,7 @@ __global__ void __launch_bounds__(NW * 32) decode_split_f32(const __grid_constan
     }
     __syncthreads();
     decode_epilogue<D, NW, HT, float>(a, red_o, red_m, red_l, b, h0, nh, s, n_splits);
-    if constexpr (WEIGHTED) write_statistics<NW, HT>(a, red_m, red_l, b, h0, nh, s);
+    if constexpr (WEIGHTED) write_statistics<NW, HT>(a, red_m, red_l, b, h0, nh, s, kvh, ctx);
 }
 
 }  // namespace pa

@@ -453,20 +453,18 @@ pa_status pa_decode_accumulate_weights(void *out, float *weights_out, const floa
     a.part_l = reinterpret_cast<float *>(ws + statistics_bytes(num_seqs, num_q_heads, S));
     a.scores = reinterpret_cast<float *>(ws + 2 * statistics_bytes(num_seqs, num_q_heads, S));
     a.score_stride = round16(max_context_len);
+    a.weights_out = weights_out;
+    a.weights_in = weights_in;
+    a.weight_stride = weights_stride;
+    a.weight_vec = weights_stride % 4 == 0 && aligned(weights_out, 16) && aligned(weights_in, 16);
+    a.weights_here = S == 1 && a.n_htiles == 1;
     st = launch_split<Span::kWeighted>(a, shape, stream);
-    if (st != PA_OK || max_context_len == 0) return st;
+    if (st != PA_OK || a.weights_here || max_context_len == 0) return st;
 
-    WeightArgs w;
-    w.weights_out = weights_out;
-    w.weights_in = weights_in;
-    w.stride = weights_stride;
-    w.vec = weights_stride % 4 == 0 && aligned(weights_out, 16) && aligned(weights_in, 16);
-    // programmatic dependent of the split kernel; the merge behind it starts
-    // when it has finished
     st = launch_dependent(decode_weights_kernel,
                           dim3((unsigned)((max_context_len + kWeightTile - 1) / kWeightTile),
                                (unsigned)num_kv_heads, (unsigned)num_seqs),
-                          kWeightThreads, 0, stream, a, w);
+                          kWeightThreads, 0, stream, a);
     if (st != PA_OK || S <= 1) return st;
     if (dtype == PA_BF16)
         return head_dim == 128 ? launch_reduce<128, __nv_bfloat16>(a, stream)
