@@ -114,6 +114,29 @@ constexpr int kDecodeWarps = 4;
 constexpr int kDecodeStages = 2;
 constexpr int kQ8Tokens = 32;
 
+// A launch as clusters of `cs` consecutive CTAs along x.
+template <typename K, typename... A>
+pa_status launch_clusters(K kernel, dim3 grid, int threads, int cs, size_t smem, cudaStream_t st,
+                          const A &...args) {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)cs;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    cfg.stream = st;
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    if (cudaLaunchKernelEx(&cfg, kernel, args...) != cudaSuccess) {
+        cudaGetLastError();
+        return PA_ERR_CUDA;
+    }
+    return launch_status();
+}
+
 // Bytes of a split CTA's table slice: block ids, and for listed blocks their
 // numbers of valid tokens.
 template <Span SPAN>
@@ -129,6 +152,7 @@ pa_status launch_decode_bf16(const DecodeArgs &a, const CUtensorMap &mk, const C
     const size_t smem = 1024 + L::kTable + slice_bytes<SPAN>(a);
     auto k = decode_split_bf16<D, NW, NS, SPAN>;
     if (set_smem(k, smem) != cudaSuccess) return PA_ERR_CUDA;
+    if (a.cluster) return launch_clusters(k, grid, NW * 32, (int)grid.x, smem, st, a, mk, mv);
     k<<<grid, NW * 32, smem, st>>>(a, mk, mv);
     return launch_status();
 }
@@ -140,6 +164,7 @@ pa_status launch_decode_f32(const DecodeArgs &a, dim3 grid, cudaStream_t st) {
     const size_t smem = 1024 + L::kTable + slice_bytes<SPAN>(a);
     auto k = decode_split_f32<D, NW, NS, SPAN>;
     if (set_smem(k, smem) != cudaSuccess) return PA_ERR_CUDA;
+    if (a.cluster) return launch_clusters(k, grid, NW * 32, (int)grid.x, smem, st, a);
     k<<<grid, NW * 32, smem, st>>>(a);
     return launch_status();
 }

@@ -230,7 +230,7 @@ def test_two_graphs_on_two_streams(pa):
 def test_binding_refuses_mismatched_tensors(pa):
     batch = appended([100, 40], 8, 2, 128, 16, BF16, 311)
     d = batch.to(DEV)
-    sel = torch.zeros(2, 2, 4, dtype=torch.int32, device=DEV)
+    sel = torch.full((2, 2, 20), -1, dtype=torch.int32, device=DEV)
     base = dict(out=torch.empty_like(d.q), q=d.q, k=d.k_cache, v=d.v_cache, t=d.block_tables,
                 n=d.context_lens, s=sel, scale=0.1, part=0, ws=None)
     call = lambda **k: pa.pa_decode_selected_blocks(*{**base, **k}.values())

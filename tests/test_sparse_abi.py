@@ -73,9 +73,11 @@ def test_select_blocks_host_checks(pa):
 def test_decode_selected_blocks_host_checks(pa):
     args = dict(out=FAKE, q=FAKE, k=FAKE, v=FAKE, tables=FAKE, lens=FAKE, sel=FAKE, K=4, B=4,
                 Hq=8, Hkv=2, **SHAPE, scale=0.1, part=0, ws=None, ws_bytes=0, dtype=1)
-    need = pa.pa_decode_selected_blocks_workspace_size(4, 8, 2, 128, 16, 4, 16)
-    o, l_ = 4 * 8 * 4 * 128 * 4, 4 * 8 * 4 * 4
-    assert need == o + l_
+    need = pa.pa_decode_selected_blocks_workspace_size(4, 8, 2, 128, 16, 9, 16)
+    o, l_ = 4 * 8 * 9 * 128 * 4, 4 * 8 * 9 * 4
+    assert need == o + -(-l_ // 256) * 256
+    # up to eight partitions are merged inside a cluster
+    assert pa.pa_decode_selected_blocks_workspace_size(4, 8, 2, 128, 16, 8, 16) == 0
     # one partition needs none; invalid sizes report none
     f = pa.pa_decode_selected_blocks_workspace_size
     assert f(4, 8, 2, 128, 16, 4, -1) == 0 and f(4, 8, 2, 128, 16, 0) == 0
@@ -86,9 +88,9 @@ def test_decode_selected_blocks_host_checks(pa):
         (dict(sel=ODD2), pa.PA_ERR_INVALID_ARG), (dict(out=ODD4), pa.PA_ERR_INVALID_ARG),
         (dict(part=24), pa.PA_ERR_INVALID_ARG), (dict(part=32768), pa.PA_ERR_INVALID_ARG),
         (dict(part=-1, K=1025), pa.PA_ERR_UNSUPPORTED), (dict(K=1 << 28), pa.PA_ERR_UNSUPPORTED),
-        (dict(part=16), pa.PA_ERR_WORKSPACE),
-        (dict(part=16, ws=FAKE, ws_bytes=need - 1), pa.PA_ERR_WORKSPACE),
-        (dict(part=16, ws=ctypes.c_void_p(0x10010), ws_bytes=need), pa.PA_ERR_WORKSPACE)])
+        (dict(part=16, K=9), pa.PA_ERR_WORKSPACE),
+        (dict(part=16, K=9, ws=FAKE, ws_bytes=need - 1), pa.PA_ERR_WORKSPACE),
+        (dict(part=16, K=9, ws=ctypes.c_void_p(0x10010), ws_bytes=need), pa.PA_ERR_WORKSPACE)])
 
 
 def test_decode_accumulate_weights_host_checks(pa):
