@@ -225,6 +225,24 @@ __device__ __forceinline__ void write_zero_rows(const DecodeArgs &a, int b, int 
     }
 }
 
+// kWeighted: K and V pass through L2 as the first to leave it, so that the
+// scores stay there for the kernel that reads them.
+__device__ __forceinline__ uint64_t read_once_policy() {
+    uint64_t p;
+    asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
+    return p;
+}
+__device__ __forceinline__ void tma_load_4d_once(uint32_t dst, const CUtensorMap *map,
+                                                 uint32_t bar, int c0, int c1, int c2, int c3,
+                                                 uint64_t policy) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        ".L2::cache_hint [%0], [%1, {%2, %3, %4, %5}], [%6], %7;" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(bar),
+        "l"(policy)
+        : "memory");
+}
+
 // kListed with few partitions: they are the CTAs of a cluster, which puts the
 // output together through distributed shared memory -- no workspace and no
 // second kernel (one row, 64 blocks of 16 tokens: 8.7 -> 6.6 us). Each CTA
@@ -515,6 +533,8 @@ __global__ void __launch_bounds__(NW * 32)
 
     const int my_n = n_chunks > warp ? (n_chunks - warp + NW - 1) / NW : 0;
     const uint32_t stage0 = sbase + warp * NS * STAGE;
+    uint64_t once = 0;
+    if constexpr (WEIGHTED) once = read_once_policy();
 
     auto issue = [&](int i) {  // lane 0: chunk i of this warp -> stage i % NS
         const int st = i % NS;
@@ -530,8 +550,14 @@ __global__ void __launch_bounds__(NW * 32)
         const int off = t & (a.bs - 1);
 #pragma unroll
         for (int sub = 0; sub < D / 64; ++sub) {
-            tma_load_4d(kdst + sub * SUBTILE, &tmk, bar, sub * 64, off, kvh, id);
-            tma_load_4d(kdst + HALF + sub * SUBTILE, &tmv, bar, sub * 64, off, kvh, id);
+            if constexpr (WEIGHTED) {
+                tma_load_4d_once(kdst + sub * SUBTILE, &tmk, bar, sub * 64, off, kvh, id, once);
+                tma_load_4d_once(kdst + HALF + sub * SUBTILE, &tmv, bar, sub * 64, off, kvh, id,
+                                 once);
+            } else {
+                tma_load_4d(kdst + sub * SUBTILE, &tmk, bar, sub * 64, off, kvh, id);
+                tma_load_4d(kdst + HALF + sub * SUBTILE, &tmv, bar, sub * 64, off, kvh, id);
+            }
         }
     };
     if (lane == 0) {
