@@ -180,6 +180,16 @@ def test_selection_of_long_rows(pa, batch):
     assert pa.pa_device_error() == 0
 
 
+@pytest.mark.parametrize("D,dtype", [(64, BF16), (128, BF16), (64, F32), (128, F32)])
+def test_selection_of_many_short_rows(pa, D, dtype):
+    ctxs = [1 + (37 * i) % 700 for i in range(320)]
+    q, bounds, tables, lens = bounds_case(ctxs, 4, 2, D, 16, dtype, 220)
+    bounds[tables[5].long()] = bounds[tables[5, 0].long()].clone()   # a row of equal blocks
+    want = R.select_blocks(q, bounds, tables, lens, 16, 9, 1, 1)
+    assert torch.equal(run_select(pa, q, bounds, tables, lens, 700, 16, 9, 1, 1), want)
+    assert pa.pa_device_error() == 0
+
+
 def test_equal_scores_go_to_the_lowest_index(pa):
     for dtype in (BF16, F32):
         q, bounds, tables, lens = bounds_case([1600, 3200], 8, 2, 128, 16, dtype, 207)
