@@ -461,7 +461,8 @@ PA_API pa_status pa_decode_selected_blocks(void *out, const void *q, const void 
                                            cudaStream_t stream);
 
 /* pa_decode that also adds up each position's attention weight:
- *   out as pa_decode's (bit for bit), and for j < context_lens[b]
+ *   out as pa_decode's (bf16, at one partition size: bit for bit), and for
+ *   j < context_lens[b]
  *   weights_out[b][h][j] = weights_in[b][h][j]
  *       + sum over the query heads g of K/V head h of
  *         softmax_j(scale * q[b][g] . K_j).
@@ -471,6 +472,8 @@ PA_API pa_status pa_decode_selected_blocks(void *out, const void *q, const void 
  *                 Positions at and past context_lens[b] are neither read nor
  *                 written, so a new token's old weight is whatever its place
  *                 holds: zero it once (pa_evict_tokens zeroes what it frees).
+ *   partition_size  as in pa_decode; 0 = automatic (smaller partitions than
+ *                 pa_decode's where there are few rows).
  *   workspace     >= pa_decode_accumulate_weights_workspace_size(...) bytes,
  *                 256-byte aligned (it holds every head's scores, 4 bytes per
  *                 query head and position); contents on entry are ignored.

@@ -385,6 +385,20 @@ __device__ __forceinline__ void clear_scores(const DecodeArgs &a, float *scores,
         scores[(size_t)(e / kChunk) * a.score_stride + t + e % kChunk] = -INFINITY;
 }
 
+// Table entries [e0, e0 + n) of row b -> tbl[0..n), checked.
+__device__ __forceinline__ void load_table(const DecodeArgs &a, int b, int e0, int n,
+                                           int32_t *tbl) {
+    const int32_t *row = a.block_tables + (size_t)b * a.MB + e0;
+    for (int i = threadIdx.x; i < n; i += blockDim.x) {
+        int id = __ldg(row + i);
+        if (id < 0 || id >= a.NB) {
+            flag_error(PA_ERR_BAD_TABLE);
+            id = -1;
+        }
+        tbl[i] = id;
+    }
+}
+
 // List entries [e0, e0 + n) of (b, kvh) -> their physical ids in tbl[0..n)
 // and their numbers of valid tokens in tbl[P / bs + 2 + 0..n).
 __device__ __forceinline__ void load_listed(const DecodeArgs &a, int b, int kvh, int ctx, int e0,
@@ -406,6 +420,22 @@ __device__ __forceinline__ void load_listed(const DecodeArgs &a, int b, int kvh,
         tbl[i] = id;
         tbl[a.P / a.bs + 2 + i] = tokens;
     }
+}
+
+// With a slice from entry lb0 on in tbl: the physical block of the chunk at
+// position t, negative when it has no valid token, and its valid tokens.
+template <bool LISTED>
+__device__ __forceinline__ int block_of_chunk(const DecodeArgs &a, const int32_t *tbl, int lb0,
+                                              int t) {
+    const int i = (t >> a.bs_shift) - lb0;
+    if (LISTED && (t & (a.bs - 1)) >= tbl[a.P / a.bs + 2 + i]) return -1;
+    return tbl[i];
+}
+template <bool LISTED>
+__device__ __forceinline__ int valid_of_chunk(const DecodeArgs &a, const int32_t *tbl, int lb0,
+                                              int t, int tok1) {
+    if (!LISTED) return min(kChunk, tok1 - t);
+    return min(kChunk, tbl[a.P / a.bs + 2 + (t >> a.bs_shift) - lb0] - (t & (a.bs - 1)));
 }
 
 // ------------------------------------------------------------------ bf16
@@ -500,30 +530,10 @@ __global__ void __launch_bounds__(NW * 32)
     const int n_tbl = ((tok1 - 1) >> a.bs_shift) - lb0 + 1;
 
     // table slice of this partition -> shared memory (ids checked once here)
-    if constexpr (LISTED) {
+    if constexpr (LISTED)
         load_listed(a, b, kvh, ctx, lb0, n_tbl, tbl);
-    } else {
-        const int32_t *row = a.block_tables + (size_t)b * a.MB + lb0;
-        for (int i = threadIdx.x; i < n_tbl; i += NW * 32) {
-            int id = __ldg(row + i);
-            if (id < 0 || id >= a.NB) {
-                flag_error(PA_ERR_BAD_TABLE);
-                id = -1;
-            }
-            tbl[i] = id;
-        }
-    }
-    // physical block of the chunk at position t, negative when it has no
-    // valid token, and the chunk's number of valid tokens
-    auto block_at = [&](int t) {
-        const int i = (t >> a.bs_shift) - lb0;
-        if (LISTED && (t & (a.bs - 1)) >= tbl[a.P / a.bs + 2 + i]) return -1;
-        return tbl[i];
-    };
-    auto valid_at = [&](int t) {
-        if (!LISTED) return min(kChunk, tok1 - t);
-        return min(kChunk, tbl[a.P / a.bs + 2 + (t >> a.bs_shift) - lb0] - (t & (a.bs - 1)));
-    };
+    else
+        load_table(a, b, lb0, n_tbl, tbl);
     const uint32_t bar0 = sbase + L::kBars + warp * NS * 8;
     if (lane == 0) {
         for (int st = 0; st < NS; ++st) mbar_init(bar0 + st * 8, 1);
@@ -540,7 +550,7 @@ __global__ void __launch_bounds__(NW * 32)
         const int st = i % NS;
         const uint32_t bar = bar0 + st * 8;
         const int t = tok0 + (warp + i * NW) * kChunk;
-        const int id = block_at(t);
+        const int id = block_of_chunk<LISTED>(a, tbl, lb0, t);
         if (id < 0) {
             mbar_arrive(bar);  // nothing to load; the chunk is skipped
             return;
@@ -602,9 +612,9 @@ __global__ void __launch_bounds__(NW * 32)
         }
         done = i + 1;
         const int t = tok0 + (warp + i * NW) * kChunk;
-        const int id = block_at(t);
+        const int id = block_of_chunk<LISTED>(a, tbl, lb0, t);
         if (id >= 0) {
-            const int valid = valid_at(t);
+            const int valid = valid_of_chunk<LISTED>(a, tbl, lb0, t, tok1);
             const int first = max(0, lo - t);  // rows before the window start
             const uint32_t kb = stage0 + st * STAGE;
             const uint32_t vb = kb + HALF;
@@ -784,11 +794,8 @@ __global__ void __launch_bounds__(NW * 32)
 }
 
 // ------------------------------------------------------------------ fp32
-template <int D, int NW, int NS, Span SPAN = Span::kOwn>
+template <int D, int NW, int NS>
 __global__ void __launch_bounds__(NW * 32) decode_split_f32(const __grid_constant__ DecodeArgs a) {
-    static_assert(SPAN != Span::kTail, "no fp32 shared-prefix decode");
-    constexpr bool LISTED = SPAN == Span::kListed;
-    constexpr bool WEIGHTED = SPAN == Span::kWeighted;
     constexpr int HT = kHeadsF32;
     constexpr int VEC = D / 32;          // dims per lane
     constexpr int HALF = kChunk * D * 4;
@@ -810,46 +817,28 @@ __global__ void __launch_bounds__(NW * 32) decode_split_f32(const __grid_constan
 
     allow_dependent_launch();
     const int ctx = clamped_ctx(a, b, s == 0 && blockIdx.y == 0 && threadIdx.x == 0);
-    const int lo = LISTED ? 0 : window_lo(a, ctx), base = LISTED ? 0 : span_base(a, ctx);
-    const int n_splits = LISTED ? a.S_max : (ctx - base + a.P - 1) / a.P;
-    if (!LISTED) {
-        if (s >= (n_splits > 0 ? n_splits : 1)) return;
-        if (ctx == 0) {
-            write_zero_rows<D, float>(a, b, h0, nh);
-            return;
-        }
+    const int lo = window_lo(a, ctx), base = span_base(a, ctx);
+    const int n_splits = (ctx - base + a.P - 1) / a.P;
+    if (s >= (n_splits > 0 ? n_splits : 1)) return;
+    if (ctx == 0) {
+        write_zero_rows<D, float>(a, b, h0, nh);
+        return;
     }
     const int tok0 = base + s * a.P;
-    const int tok1 = min(tok0 + a.P, LISTED ? a.n_listed << a.bs_shift : ctx);
+    const int tok1 = min(tok0 + a.P, ctx);
     const int n_chunks = (tok1 - tok0 + kChunk - 1) / kChunk;
     const int lb0 = tok0 >> a.bs_shift;
     const int n_tbl = ((tok1 - 1) >> a.bs_shift) - lb0 + 1;
 
-    // table slice of this partition -> shared memory (ids checked once here)
-    if constexpr (LISTED) {
-        load_listed(a, b, kvh, ctx, lb0, n_tbl, tbl);
-    } else {
-        const int32_t *row = a.block_tables + (size_t)b * a.MB + lb0;
-        for (int i = threadIdx.x; i < n_tbl; i += NW * 32) {
-            int id = __ldg(row + i);
-            if (id < 0 || id >= a.NB) {
-                flag_error(PA_ERR_BAD_TABLE);
-                id = -1;
-            }
-            tbl[i] = id;
+    const int32_t *row = a.block_tables + (size_t)b * a.MB + lb0;
+    for (int i = threadIdx.x; i < n_tbl; i += NW * 32) {
+        int id = __ldg(row + i);
+        if (id < 0 || id >= a.NB) {
+            flag_error(PA_ERR_BAD_TABLE);
+            id = -1;
         }
+        tbl[i] = id;
     }
-    // physical block of the chunk at position t, negative when it has no
-    // valid token, and the chunk's number of valid tokens
-    auto block_at = [&](int t) {
-        const int i = (t >> a.bs_shift) - lb0;
-        if (LISTED && (t & (a.bs - 1)) >= tbl[a.P / a.bs + 2 + i]) return -1;
-        return tbl[i];
-    };
-    auto valid_at = [&](int t) {
-        if (!LISTED) return min(kChunk, tok1 - t);
-        return min(kChunk, tbl[a.P / a.bs + 2 + (t >> a.bs_shift) - lb0] - (t & (a.bs - 1)));
-    };
     const uint32_t bar0 = sbase + L::kBars + warp * NS * 8;
     if (lane == 0) {
         for (int st = 0; st < NS; ++st) mbar_init(bar0 + st * 8, 1);
@@ -866,7 +855,7 @@ __global__ void __launch_bounds__(NW * 32) decode_split_f32(const __grid_constan
         const int st = i % NS;
         const uint32_t bar = bar0 + st * 8;
         const int t = tok0 + (warp + i * NW) * kChunk;
-        const int id = block_at(t);
+        const int id = tbl[(t >> a.bs_shift) - lb0];
         if (id < 0) {
             mbar_arrive(bar);
             return;
@@ -894,8 +883,6 @@ __global__ void __launch_bounds__(NW * 32) decode_split_f32(const __grid_constan
             lrow[g] = 0.f;
         }
     }
-    float *scores = nullptr;
-    if constexpr (WEIGHTED) scores = a.scores + ((size_t)b * a.H_q + h0) * a.score_stride;
     int done = 0;
     bool failed = false;
     for (int i = 0; i < my_n; ++i) {
@@ -909,9 +896,9 @@ __global__ void __launch_bounds__(NW * 32) decode_split_f32(const __grid_constan
         }
         done = i + 1;
         const int t = tok0 + (warp + i * NW) * kChunk;
-        const int id = block_at(t);
+        const int id = tbl[(t >> a.bs_shift) - lb0];
         if (id >= 0) {
-            const int valid = valid_at(t);
+            const int valid = min(kChunk, tok1 - t);
             const int first = max(0, lo - t);
             const float *ks = reinterpret_cast<const float *>(smem + warp * NS * STAGE + st * STAGE);
             const float *vs = ks + kChunk * D;
@@ -929,7 +916,6 @@ __global__ void __launch_bounds__(NW * 32) decode_split_f32(const __grid_constan
 #pragma unroll
                         for (int v = 0; v < VEC; ++v) dot = fmaf(qv[g][v], kk[v], dot);
                         const float sc = warp_sum(dot) * a.scale_log2;
-                        if (WEIGHTED && lane == 0) scores[(size_t)g * a.score_stride + t + j] = sc;
                         const float mn = fmaxf(mrow[g], sc);
                         const float c = exp2f(mrow[g] - mn);
                         const float p = exp2f(sc - mn);
@@ -940,8 +926,6 @@ __global__ void __launch_bounds__(NW * 32) decode_split_f32(const __grid_constan
                     }
                 }
             }
-        } else if constexpr (WEIGHTED) {
-            clear_scores(a, scores, t, nh, lane);
         }
         __syncwarp();
         if (lane == 0 && i + NS < my_n) {
@@ -971,14 +955,7 @@ __global__ void __launch_bounds__(NW * 32) decode_split_f32(const __grid_constan
         for (int v = 0; v < VEC; ++v) red_o[(warp * HT + g) * OS + lane * VEC + v] = acc[g][v];
     }
     __syncthreads();
-    if (LISTED && a.cluster) {
-        static_assert(!LISTED || L::kMerge + (2 * HT + HT * D) * 4 <= L::kStages, "room");
-        cluster_epilogue<D, NW, HT, float>(a, red_o, red_m, red_l,
-                                           reinterpret_cast<float *>(smem + L::kMerge), b, h0, nh);
-        return;
-    }
     decode_epilogue<D, NW, HT, float>(a, red_o, red_m, red_l, b, h0, nh, s, n_splits);
-    if constexpr (WEIGHTED) write_statistics<NW, HT>(a, red_m, red_l, b, h0, nh, s, kvh, ctx);
 }
 
 }  // namespace pa

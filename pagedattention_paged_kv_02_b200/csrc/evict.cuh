@@ -48,6 +48,8 @@ struct EvictArgs {
     int budget, first, last;
     int row_bytes;            // D * element size
     int parts;                // CTAs that share a (row, K/V head)'s K, and its V
+    int columns;              // of them, those that take columns where order matters
+    int weight_parts;         // CTAs that share its weights
     int stage;                // weights of a segment that fit shared memory
 };
 
@@ -235,6 +237,25 @@ __global__ void __launch_bounds__(T)
             atomicMax(&sm.hi, hi);
         }
         cluster.sync();
+        if (ranks == 1 && count <= T) {
+            // few weights: a thread each, in when fewer than `need` rank before
+            // it (larger, or equal and earlier)
+            const uint32_t k = tid < count ? evict_keys[tid] : 0;
+            uint32_t before = 0;
+            const uint4 *quads = reinterpret_cast<const uint4 *>(evict_keys);
+            for (int i = 0; i < (count + 3) / 4; ++i) {  // (0 past the end ranks last)
+                const uint4 x = quads[i];
+                before += x.x > k || (x.x == k && 4 * i < tid);
+                before += x.y > k || (x.y == k && 4 * i + 1 < tid);
+                before += x.z > k || (x.z == k && 4 * i + 2 < tid);
+                before += x.w > k || (x.w == k && 4 * i + 3 < tid);
+            }
+            const bool in = tid < count && before < need;
+            uint32_t all;
+            const uint32_t place = block_before<T>(sm.row, in, all);
+            if (in) emit((int)place, tid);
+            return;
+        }
         done = staged_cut<T>(cluster, sm, evict_keys, count, need, cut);
     }
     if (done) {
@@ -257,8 +278,6 @@ __global__ void __launch_bounds__(T)
     cluster.sync();  // no CTA exits while another may read its shared memory
 }
 
-constexpr int kMoveThreads = 256;
-constexpr int kMoveLoads = 8;  // 16-byte loads a thread has in flight
 
 __device__ __forceinline__ uint4 load_row(const char *p) {
     uint4 x;
@@ -269,36 +288,45 @@ __device__ __forceinline__ uint4 load_row(const char *p) {
     return x;
 }
 
-// Grid: (parts of K, parts of V, weights; K/V head; row).
-__global__ void __launch_bounds__(kMoveThreads)
+// Grid: (parts of K, parts of V, parts of the weights; K/V head; row). A chunk is
+// U 16-byte loads of each of T threads.
+template <int T, int U>
+__global__ void __launch_bounds__(T)
     evict_move_kernel(const __grid_constant__ EvictArgs a) {
-    constexpr int U = kMoveLoads;
-    constexpr int kMaxChunk = kMoveThreads / 4 * U;  // a token's part has 64 bytes or more
+    constexpr int kMaxChunk = T / 4 * U;  // a token's part has 64 bytes or more
     __shared__ long long from[2][kMaxChunk], to[2][kMaxChunk];
     const int h = blockIdx.y, b = blockIdx.z;
     const int n = evict_len(a, b, false);
     const int kept = min(n, a.budget);
     const int32_t *pos = a.kept + (size_t)((long long)b * a.H_kv + h) * a.budget;
 
-    if ((int)blockIdx.x == 2 * a.parts) {  // the weights
+    if ((int)blockIdx.x >= 2 * a.parts) {  // the weights
+        constexpr int W = 8;               // of a chunk, per thread
         const size_t row = (size_t)((long long)b * a.H_kv + h) * a.stride;
         const float *in = a.weights_in + row;
         float *out = a.weights_out + row;
-        for (int c0 = 0; c0 < kept; c0 += kMoveThreads * U) {
-            float x[U];
+        // in place there is an order, as for the columns: one CTA keeps it
+        const int part = (int)blockIdx.x - 2 * a.parts;
+        const int parts = a.weights_in == a.weights_out ? 1 : a.weight_parts;
+        if (part >= parts) return;
+        const int run = (n + parts - 1) / parts;
+        const int begin = min(part * run, n), end = min(begin + run, n);
+        const int moved = min(end, kept);
+        for (int c0 = begin; c0 < moved; c0 += T * W) {
+            float x[W];
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int i = c0 + u * kMoveThreads + threadIdx.x;
-                if (i < kept) x[u] = in[pos[i]];
+            for (int u = 0; u < W; ++u) {
+                const int i = c0 + u * T + threadIdx.x;
+                if (i < moved) x[u] = in[pos[i]];
             }
             __syncthreads();
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int i = c0 + u * kMoveThreads + threadIdx.x;
-                if (i < kept) out[i] = x[u];
+            for (int u = 0; u < W; ++u) {
+                const int i = c0 + u * T + threadIdx.x;
+                if (i < moved) out[i] = x[u];
             }
         }
-        for (int i = kept + threadIdx.x; i < n; i += kMoveThreads) out[i] = 0.f;
+        for (int i = max(begin, kept) + threadIdx.x; i < end; i += T) out[i] = 0.f;
         return;
     }
 
@@ -307,21 +335,23 @@ __global__ void __launch_bounds__(kMoveThreads)
     const bool is_v = (int)blockIdx.x >= a.parts;
     const int part = (int)blockIdx.x - (is_v ? a.parts : 0);
     bool stays = false;  // some block is its own destination
-    for (int i = threadIdx.x; i < (kept + a.bs - 1) >> a.bs_shift; i += kMoveThreads)
+    for (int i = threadIdx.x; i < (kept + a.bs - 1) >> a.bs_shift; i += T)
         stays |= __ldg(src_row + i) == __ldg(dst_row + i);
     const bool columns = __syncthreads_or(stays) != 0;
-    const int width = columns ? a.row_bytes / a.parts : a.row_bytes;
+    const int parts = columns ? a.columns : a.parts;
+    if (part >= parts) return;
+    const int width = columns ? a.row_bytes / parts : a.row_bytes;
     const int per_row = width >> 4;                // threads on one token, a power of two
-    const int rows = kMoveThreads / per_row;
+    const int rows = T / per_row;
     const int chunk = rows * U;                    // tokens
     const int r0 = threadIdx.x / per_row;
-    const int run = columns ? kept : (kept + a.parts - 1) / a.parts;
+    const int run = columns ? kept : (kept + parts - 1) / parts;
     const int begin = columns ? 0 : min(part * run, kept), end = min(begin + run, kept);
     char *cache = (is_v ? a.v_cache : a.k_cache) + (columns ? (size_t)part * width : 0) +
                   (size_t)(threadIdx.x % per_row) * 16;
     // cache rows the chunk's tokens come from and go to, -1 for one that stays
     auto locate = [&](int c0, int half) {
-        for (int i = threadIdx.x; i < chunk; i += kMoveThreads) {
+        for (int i = threadIdx.x; i < chunk; i += T) {
             long long s = -1, d = -1;
             if (c0 + i < end) {
                 const int p = pos[c0 + i], q = c0 + i;

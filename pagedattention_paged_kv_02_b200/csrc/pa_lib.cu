@@ -19,6 +19,7 @@
 #include "pa_device.cuh"
 #include "reshape_and_cache.cuh"
 #include "decode.cuh"
+#include "decode_f32.cuh"
 #include "decode_merge.cuh"
 #include "decode_prefix.cuh"
 #include "decode_fp8.cuh"
@@ -157,14 +158,13 @@ pa_status launch_decode_bf16(const DecodeArgs &a, const CUtensorMap &mk, const C
     return launch_status();
 }
 
-template <int D, int NW, int NS, Span SPAN = Span::kOwn>
+template <int D, int NW, int NS>
 pa_status launch_decode_f32(const DecodeArgs &a, dim3 grid, cudaStream_t st) {
     constexpr int STAGE = 2 * kChunk * D * 4;
     using L = DecodeSmem<NW, NS, STAGE, kHeadsF32, D>;
-    const size_t smem = 1024 + L::kTable + slice_bytes<SPAN>(a);
-    auto k = decode_split_f32<D, NW, NS, SPAN>;
+    const size_t smem = 1024 + L::kTable + slice_bytes<Span::kOwn>(a);
+    auto k = decode_split_f32<D, NW, NS>;
     if (set_smem(k, smem) != cudaSuccess) return PA_ERR_CUDA;
-    if (a.cluster) return launch_clusters(k, grid, NW * 32, (int)grid.x, smem, st, a);
     k<<<grid, NW * 32, smem, st>>>(a);
     return launch_status();
 }

@@ -52,20 +52,25 @@ int cluster_size(long long rows, long long items, int grain) {
     return cs;
 }
 
-// KV tokens per partition of a decode over n_listed blocks, or -1. Automatic:
-// up to 1024 tokens, halved while the grid has fewer than two CTAs per SM and
-// a partition keeps more than 128 tokens.
-int listed_partition(int n_listed, int bs, long long rows, int partition_size) {
-    const long long total = (long long)n_listed * bs;
+// KV tokens per partition of these decodes over `total` tokens a row, or -1.
+// Automatic: up to 1024 tokens, halved while the grid has fewer than two CTAs
+// per SM and a partition keeps more than 128 tokens (a partition's tokens are a
+// chain of 64 per step of its four warps: 1024 of them take about 20 us).
+int spread_partition(long long total, long long rows, int partition_size) {
     if (total <= 0 || total > 0x7fffffffLL) return -1;
     if (partition_size > 0)
         return partition_size % kChunk != 0 || partition_size > kMaxPartition ? -1 : partition_size;
-    if (partition_size < 0) return total <= kMaxPartition ? (int)total : -1;
-    int P = total <= 1024 ? (int)total : 1024;
+    const int whole = round16((int)std::min(total, 1LL << 30));
+    if (partition_size < 0) return whole <= kMaxPartition ? whole : -1;
+    int P = std::min(whole, 1024);
     while (rows * ((total + P - 1) / P) < 2 * 148 && P > 128) P = round16(P / 2);
     return P;
 }
+int listed_partition(int n_listed, int bs, long long rows, int partition_size) {
+    return spread_partition((long long)n_listed * bs, rows, partition_size);
+}
 
+// (Row, K/V head, tile of query heads) triples of a grid.
 long long listed_rows(int num_seqs, int num_q_heads, int num_kv_heads) {
     const int group = num_q_heads / num_kv_heads;
     return (long long)num_seqs * num_kv_heads * ((group + kHeadsBf16 - 1) / kHeadsBf16);
@@ -135,6 +140,24 @@ void fill_decode(DecodeArgs &a, const DecodeShape &s, void *out, const void *q,
     a.timeout_ns = kWaitTimeoutNs;
 }
 
+template <int D, int HT, Span SPAN>
+pa_status launch_rows_f32_tile(const DecodeArgs &a, dim3 grid, cudaStream_t st) {
+    const size_t smem = 1024 + F32Smem<D, HT>::kTable + slice_bytes<SPAN>(a);
+    auto k = decode_rows_f32<D, HT, SPAN>;
+    if (set_smem(k, smem) != cudaSuccess) return PA_ERR_CUDA;
+    if (a.cluster) return launch_clusters(k, grid, kF32Warps * 32, (int)grid.x, smem, st, a);
+    k<<<grid, kF32Warps * 32, smem, st>>>(a);
+    return launch_status();
+}
+
+// A tile of 1, 4 or 8 query heads, whichever wastes the least of it.
+template <int D, Span SPAN>
+pa_status launch_rows_f32(const DecodeArgs &a, dim3 grid, cudaStream_t st) {
+    return a.group == 1   ? launch_rows_f32_tile<D, 1, SPAN>(a, grid, st)
+           : a.group <= 4 ? launch_rows_f32_tile<D, 4, SPAN>(a, grid, st)
+                          : launch_rows_f32_tile<D, 8, SPAN>(a, grid, st);
+}
+
 template <Span SPAN>
 pa_status launch_split(const DecodeArgs &a, const DecodeShape &s, cudaStream_t stream) {
     const dim3 grid((unsigned)a.S_max, (unsigned)(a.H_kv * a.n_htiles), (unsigned)a.num_seqs);
@@ -149,9 +172,8 @@ pa_status launch_split(const DecodeArgs &a, const DecodeShape &s, cudaStream_t s
                    : launch_decode_bf16<64, kDecodeWarps, kDecodeStages, SPAN>(a, mk, mv, grid,
                                                                                stream);
     }
-    return s.head_dim == 128
-               ? launch_decode_f32<128, kDecodeWarps, kDecodeStages, SPAN>(a, grid, stream)
-               : launch_decode_f32<64, kDecodeWarps, kDecodeStages, SPAN>(a, grid, stream);
+    return s.head_dim == 128 ? launch_rows_f32<128, SPAN>(a, grid, stream)
+                             : launch_rows_f32<64, SPAN>(a, grid, stream);
 }
 
 // Checks of the arguments that both decode forms below share, in pa_decode's
@@ -271,7 +293,8 @@ pa_status pa_select_blocks(int32_t *selected, const void *q, const void *key_bou
     if (need > 0 && (!workspace || workspace_bytes_given < need || !aligned(workspace, 256)))
         return PA_ERR_WORKSPACE;
     // several tiles to a warp once the grid fills the GPU several times over
-    const long long all_tiles = (blocks + kScoreRows - 1) / kScoreRows;
+    const int tile = dtype == PA_BF16 ? kScoreRows : kScoreRowsF32;
+    const long long all_tiles = (blocks + tile - 1) / tile;
     int steps = 1;
     while (steps < 4 && (long long)num_seqs * num_kv_heads * all_tiles >
                             8LL * 148 * 4 * kScoreWarps * steps)
@@ -396,9 +419,11 @@ pa_status pa_decode_selected_blocks(void *out, const void *q, const void *k_cach
 
 size_t pa_decode_accumulate_weights_workspace_size(int num_seqs, int num_q_heads, int head_dim,
                                                    int max_context_len, int partition_size) {
-    const int P = partition_tokens(max_context_len, partition_size);
-    if (P <= 0 || num_seqs <= 0 || num_q_heads <= 0 || head_dim <= 0 || max_context_len == 0)
-        return 0;
+    if (num_seqs <= 0 || num_q_heads <= 0 || head_dim <= 0 || max_context_len <= 0) return 0;
+    // the fewest rows that these query heads can make, and so the most partitions
+    const long long rows = (long long)num_seqs * ((num_q_heads + kHeadsBf16 - 1) / kHeadsBf16);
+    const int P = spread_partition(max_context_len, rows, partition_size);
+    if (P <= 0) return 0;
     const long long S = ((long long)max_context_len + P - 1) / P;
     return partial_bytes(num_seqs, num_q_heads, head_dim, S) +
            2 * statistics_bytes(num_seqs, num_q_heads, S) +
@@ -422,7 +447,9 @@ pa_status pa_decode_accumulate_weights(void *out, float *weights_out, const floa
     if ((long long)max_context_len > (long long)max_blocks_per_seq * block_size ||
         weights_stride < max_context_len)
         return PA_ERR_INVALID_ARG;
-    const int P = partition_tokens(max_context_len, partition_size);
+    const int P = spread_partition(std::max(max_context_len, 1),
+                                   listed_rows(num_seqs, num_q_heads, num_kv_heads),
+                                   partition_size);
     if (P <= 0) return partition_size > 0 ? PA_ERR_INVALID_ARG : PA_ERR_UNSUPPORTED;
     if (num_seqs == 0) return PA_OK;
     if (!decode_pointers_ok(out, q, k_cache, v_cache, block_tables, context_lens) ||
@@ -547,12 +574,25 @@ pa_status pa_evict_tokens(void *k_cache, void *v_cache, float *weights_out,
         r = launch_status();
     }
     if (r != PA_OK) return r;
-    // more parts, down to columns of 64 bytes, until there are four CTAs per SM
+    // CTAs of a (row, K/V head)'s K and of its V: as many as the GPU holds at a
+    // time (two per SM; four 16K-token rows of 8 heads: 130 us, 138 with four
+    // times as many) and as have 64 tokens, or a column of 64 bytes; the same
+    // for its weights and runs of 8192
+    const int most = std::min(budget, max_context_len);
+    a.columns = a.row_bytes / 64;
     a.parts = 1;
-    while (a.row_bytes / a.parts > 64 && 2 * rows * a.parts < 4 * 148) a.parts *= 2;
-    evict_move_kernel<<<dim3((unsigned)(2 * a.parts + 1), (unsigned)num_kv_heads,
-                             (unsigned)num_seqs),
-                        kMoveThreads, 0, stream>>>(a);
+    while (4 * rows * a.parts <= 2 * 148 && a.parts < std::max(a.columns, most / 64)) a.parts *= 2;
+    a.columns = std::min(a.columns, a.parts);
+    a.weight_parts = 1;
+    while (rows * a.weight_parts < 148 && a.weight_parts * 8192LL < max_context_len)
+        a.weight_parts *= 2;
+    const dim3 move_grid((unsigned)(2 * a.parts + a.weight_parts), (unsigned)num_kv_heads,
+                         (unsigned)num_seqs);
+    // small CTAs, and more of them on an SM, where a CTA has little to move
+    if ((long long)most * (a.row_bytes / 16) <= 1024)
+        evict_move_kernel<64, 4><<<move_grid, 64, 0, stream>>>(a);
+    else
+        evict_move_kernel<256, 8><<<move_grid, 256, 0, stream>>>(a);
     return launch_status();
 }
 

@@ -64,7 +64,8 @@
 namespace pa {
 
 constexpr int kScoreWarps = 4;
-constexpr int kScoreRows = 16;     // blocks per warp and step
+constexpr int kScoreRows = 16;     // blocks per warp and step, bf16
+constexpr int kScoreRowsF32 = 4;   // fp32
 constexpr int kBins = kCutBins;
 constexpr int kFewBlocks = 256;    // blocks near the border ranked by pairs
 
@@ -77,7 +78,7 @@ struct SelectArgs {
     uint64_t *scores;   // [B][H_kv][max_blocks]: order key of the score << 32 | error bound
     int H_q, H_kv, group, bs, bs_shift, NB, MB, max_ctx;
     int K, first, last, max_blocks;
-    int tiles;          // 16-block tiles of a row that are scored at once
+    int tiles;          // tiles of a row (16 or 4 blocks) that are scored at once
     int stage;          // blocks whose scores fit the selecting CTA's shared memory
 };
 
@@ -264,8 +265,8 @@ __global__ void __launch_bounds__(kScoreWarps * 32)
     uint64_t *out = a.scores + ((size_t)b * a.H_kv + h) * a.max_blocks;
     const float *q =
         reinterpret_cast<const float *>(a.q) + ((size_t)b * a.H_q + (size_t)h * a.group) * D;
-    for (int i0 = first_tile * kScoreRows; i0 < middle; i0 += a.tiles * kScoreRows) {
-        const int end = min(middle, i0 + kScoreRows);
+    for (int i0 = first_tile * kScoreRowsF32; i0 < middle; i0 += a.tiles * kScoreRowsF32) {
+        const int end = min(middle, i0 + kScoreRowsF32);
 #pragma unroll 2
         for (int i = i0; i < end; ++i) {
             const int id = __ldg(table + i);
@@ -282,6 +283,7 @@ __global__ void __launch_bounds__(kScoreWarps * 32)
             load_vec<VEC>(p, lo);
             load_vec<VEC>(p + D, hi);
             float best = -INFINITY, size = 0.f;
+#pragma unroll 4
             for (int g = 0; g < a.group; ++g) {
                 load_vec<VEC>(q + (size_t)g * D + lane * VEC, x);
                 float s = 0.f, m = 0.f;

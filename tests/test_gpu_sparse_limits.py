@@ -112,7 +112,8 @@ def test_selection_over_more_blocks_than_shared_memory_holds(pa):
 
 def kept_of(pa, w, budget, first, last, lens=None):
     """Kept positions for weights alone: every block of the rows is block 0, the
-    destinations are blocks of their own."""
+    destinations are blocks of their own. The moved weights are checked here, in
+    another buffer and in place."""
     B, H, n = w.shape
     bs = 64
     need = -(-budget // bs)
@@ -122,9 +123,15 @@ def kept_of(pa, w, budget, first, last, lens=None):
     kept = torch.full((B, H, budget), -9, dtype=torch.int32, device=DEV)
     nl = torch.empty(B, dtype=torch.int32, device=DEV)
     lens = torch.full((B,), n, dtype=torch.int32) if lens is None else lens
-    pa.pa_evict_tokens(k, k.clone(), torch.empty_like(w), w, kept, nl, src, dst, lens.to(DEV), n,
-                       budget, first, last)
+    out = torch.full_like(w, 5.0)
+    same = w.clone()
+    for w_out, w_in in ((out, w), (same, same)):
+        pa.pa_evict_tokens(k, k.clone(), w_out, w_in, kept, nl, src, dst, lens.to(DEV), n, budget,
+                           first, last)
     torch.cuda.synchronize()
+    want = torch.zeros_like(w)
+    want[:, :, :budget] = w.gather(2, kept.long())
+    assert torch.equal(out, want) and torch.equal(same, want)
     return kept.cpu()
 
 
