@@ -467,8 +467,9 @@ PA_API pa_status pa_decode_selected_blocks(void *out, const void *q, const void 
  *       + sum over the query heads g of K/V head h of
  *         softmax_j(scale * q[b][g] . K_j).
  *   weights_out, weights_in   fp32 [num_seqs][num_kv_heads][weights_stride],
- *                 weights_stride >= max_context_len. weights_in may be NULL
- *                 (zeros) or weights_out itself; other overlaps are refused.
+ *                 weights_stride >= max_context_len (at most 2^30). weights_in
+ *                 may be NULL (zeros) or weights_out itself; other overlaps are
+ *                 refused.
  *                 Positions at and past context_lens[b] are neither read nor
  *                 written, so a new token's old weight is whatever its place
  *                 holds: zero it once (pa_evict_tokens zeroes what it frees).
@@ -523,7 +524,8 @@ PA_API pa_status pa_decode_accumulate_weights(void *out, float *weights_out,
  *                 buffers that do not overlap.
  *   budget        > 0; num_first + num_last <= budget; the destination table
  *                 must hold min(budget, max_context_len) tokens.
- *   max_context_len  host-side upper bound of context_lens, as in pa_decode.
+ *   max_context_len  host-side upper bound of context_lens, as in pa_decode; at
+ *                 most 2^30.
  * new_context_lens and context_lens must not overlap. A token whose source or
  * destination block id is outside the pool is not moved and recorded as
  * PA_ERR_BAD_TABLE. Two launches on `stream`. */

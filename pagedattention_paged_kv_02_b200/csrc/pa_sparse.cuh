@@ -18,6 +18,8 @@ pa_status check_cache_shape(int num_seqs, int num_kv_heads, int head_dim, int bl
     return PA_OK;
 }
 
+constexpr int kMaxPositions = 1 << 30;  // of a row's weights: sums of positions stay in an int
+
 constexpr int kSelectStage = 24576;  // scores a selecting CTA keeps in shared memory, at most
 
 constexpr int kEvictStage = 40960;   // weights a selecting CTA keeps in shared memory, at most
@@ -419,7 +421,9 @@ pa_status pa_decode_selected_blocks(void *out, const void *q, const void *k_cach
 
 size_t pa_decode_accumulate_weights_workspace_size(int num_seqs, int num_q_heads, int head_dim,
                                                    int max_context_len, int partition_size) {
-    if (num_seqs <= 0 || num_q_heads <= 0 || head_dim <= 0 || max_context_len <= 0) return 0;
+    if (num_seqs <= 0 || num_q_heads <= 0 || head_dim <= 0 || max_context_len <= 0 ||
+        max_context_len > kMaxPositions)
+        return 0;
     // the fewest rows that these query heads can make, and so the most partitions
     const long long rows = (long long)num_seqs * ((num_q_heads + kHeadsBf16 - 1) / kHeadsBf16);
     const int P = spread_partition(max_context_len, rows, partition_size);
@@ -447,6 +451,7 @@ pa_status pa_decode_accumulate_weights(void *out, float *weights_out, const floa
     if ((long long)max_context_len > (long long)max_blocks_per_seq * block_size ||
         weights_stride < max_context_len)
         return PA_ERR_INVALID_ARG;
+    if (max_context_len > kMaxPositions) return PA_ERR_UNSUPPORTED;
     const int P = spread_partition(std::max(max_context_len, 1),
                                    listed_rows(num_seqs, num_q_heads, num_kv_heads),
                                    partition_size);
@@ -516,6 +521,7 @@ pa_status pa_evict_tokens(void *k_cache, void *v_cache, float *weights_out,
     if ((long long)max_context_len > (long long)max_blocks_per_seq * block_size ||
         std::min(budget, max_context_len) > (long long)dst_max_blocks_per_seq * block_size)
         return PA_ERR_INVALID_ARG;
+    if (max_context_len > kMaxPositions) return PA_ERR_UNSUPPORTED;
     if (num_seqs == 0) return PA_OK;
     if (!k_cache || !v_cache || !weights_out || !weights_in || !kept_positions ||
         !new_context_lens || !block_tables || !dst_block_tables || !context_lens)

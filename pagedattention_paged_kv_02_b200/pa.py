@@ -562,7 +562,6 @@ class PreparedOn(Prepared):
     def __init__(self, fn: str, tensors, args):
         super().__init__(fn, args)
         self._tensors = [t for t in tensors if t is not None]
-        self.workspace = tensors[-1]  # of the calls that have one
         devices = {t.device for t in self._tensors}
         if len(devices) != 1:
             raise ValueError(f"{fn}: all tensors must be on one device")
@@ -640,7 +639,8 @@ def prepare_select_blocks(selected, q, key_bounds, block_tables, context_lens,
                           num_last: int = 0,
                           workspace: Optional[torch.Tensor] = None) -> Prepared:
     """``pa_select_blocks`` with its arguments marshalled once. Without a
-    ``workspace`` the prepared call gets one of its own."""
+    ``workspace`` the prepared call gets one of its own (so, like any prepared
+    call with a workspace, it must not overlap itself on two streams)."""
     _check_int(selected, torch.int32, "selected")
     B, MB = _rows(block_tables, (context_lens,), ("context_lens",))
     NB, H_kv, D = _bounds_shape(key_bounds)
@@ -653,12 +653,14 @@ def prepare_select_blocks(selected, q, key_bounds, block_tables, context_lens,
     if workspace is None:
         n = pa_select_blocks_workspace_size(B, H_kv, block_size, max_context_len)
         workspace = torch.empty(n, dtype=torch.uint8, device=q.device)
-    return PreparedOn("pa_select_blocks",
+    call = PreparedOn("pa_select_blocks",
                       (selected, q, key_bounds, block_tables, context_lens, workspace),
                       (_p(selected), _p(q), _p(key_bounds), _p(block_tables), _p(context_lens),
                        selected.shape[2], int(num_first), int(num_last), B, q.shape[1], H_kv, D,
                        int(block_size), NB, MB, int(max_context_len), _p(workspace),
                        _nbytes(workspace), _dt(q)))
+    call.workspace = workspace
+    return call
 
 
 def pa_select_blocks(selected, q, key_bounds, block_tables, context_lens, max_context_len: int,

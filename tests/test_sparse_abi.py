@@ -104,6 +104,8 @@ def test_decode_accumulate_weights_host_checks(pa):
     assert f(4, 8, 128, 100, 16) == pa.pa_decode_workspace_size(4, 8, 128, 100, 16) + \
         2 * 1024 + 4 * 8 * 112 * 4
     assert f(0, 8, 128, 128) == 0 and f(4, 8, 128, 0) == 0 and f(4, 8, 128, 128, 24) == 0
+    assert f(1, 8, 128, (1 << 30) + 1) == 0
+    long = dict(MB=(1 << 26) + 1, max_ctx=(1 << 30) + 1, stride=(1 << 30) + 1)
     near = ctypes.c_void_p(0x10000 + 64)
     refusals(pa, "pa_decode_accumulate_weights", args, common_cases(pa) + [
         (dict(Hq=7), pa.PA_ERR_UNSUPPORTED), (dict(max_ctx=129, stride=256), pa.PA_ERR_INVALID_ARG),
@@ -111,6 +113,7 @@ def test_decode_accumulate_weights_host_checks(pa):
         (dict(scale=float("inf")), pa.PA_ERR_INVALID_ARG), (dict(wo=None), pa.PA_ERR_INVALID_ARG),
         (dict(wo=ODD2), pa.PA_ERR_INVALID_ARG), (dict(wi=ODD2), pa.PA_ERR_INVALID_ARG),
         (dict(wi=near), pa.PA_ERR_INVALID_ARG), (dict(part=24), pa.PA_ERR_INVALID_ARG),
+        (long, pa.PA_ERR_UNSUPPORTED),
         (dict(), pa.PA_ERR_WORKSPACE), (dict(ws=None, ws_bytes=need), pa.PA_ERR_WORKSPACE),
         (dict(ws=ctypes.c_void_p(0x10010), ws_bytes=need), pa.PA_ERR_WORKSPACE)])
 
@@ -128,6 +131,8 @@ def test_evict_tokens_host_checks(pa):
         (dict(dst_MB=0), pa.PA_ERR_INVALID_ARG), (dict(dst_MB=3), pa.PA_ERR_INVALID_ARG),
         (dict(max_ctx=129, stride=200), pa.PA_ERR_INVALID_ARG),
         (dict(max_ctx=-1), pa.PA_ERR_INVALID_ARG), (dict(stride=127), pa.PA_ERR_INVALID_ARG),
+        (dict(MB=(1 << 26) + 1, max_ctx=(1 << 30) + 1, stride=(1 << 30) + 1),
+         pa.PA_ERR_UNSUPPORTED),
         (dict(new=FAKE), pa.PA_ERR_INVALID_ARG), (dict(new=ODD4), pa.PA_ERR_INVALID_ARG),
         (dict(wi=ctypes.c_void_p(0x10040)), pa.PA_ERR_INVALID_ARG),
         (dict(wi=None), pa.PA_ERR_INVALID_ARG), (dict(kept=None), pa.PA_ERR_INVALID_ARG),
