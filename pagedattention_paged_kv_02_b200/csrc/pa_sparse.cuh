@@ -582,15 +582,16 @@ pa_status pa_evict_tokens(void *k_cache, void *v_cache, float *weights_out,
     if (r != PA_OK) return r;
     // CTAs of a (row, K/V head)'s K and of its V: as many as the GPU holds at a
     // time (two per SM; four 16K-token rows of 8 heads: 130 us, 138 with four
-    // times as many) and as have 64 tokens, or a column of 64 bytes; the same
-    // for its weights and runs of 8192
+    // times as many) and as have 64 tokens, or a column of 64 bytes; then of its
+    // weights, in runs of 8192 or more
     const int most = std::min(budget, max_context_len);
     a.columns = a.row_bytes / 64;
     a.parts = 1;
     while (4 * rows * a.parts <= 2 * 148 && a.parts < std::max(a.columns, most / 64)) a.parts *= 2;
     a.columns = std::min(a.columns, a.parts);
     a.weight_parts = 1;
-    while (rows * a.weight_parts < 148 && a.weight_parts * 8192LL < max_context_len)
+    while (2 * rows * (a.parts + a.weight_parts) <= 2 * 148 &&
+           a.weight_parts * 8192LL < max_context_len)
         a.weight_parts *= 2;
     const dim3 move_grid((unsigned)(2 * a.parts + a.weight_parts), (unsigned)num_kv_heads,
                          (unsigned)num_seqs);
