@@ -27,6 +27,12 @@
  *      over the paged cache; attention within the prompt is causal (page
  *      "LLM推理优化", section 2.3, causal=True).
  *
+ *  pa_update_key_bounds, pa_select_blocks, pa_decode_selected_blocks,
+ *  pa_decode_accumulate_weights, pa_evict_tokens
+ *      page "字节跳动 AI Infra (2)", algorithm-level table, sparse attention
+ *      row, and KV table, H2O row: attend to the important tokens only, or
+ *      keep only those cached.
+ *
  * Data layout (all device memory, row-major, owned by the caller):
  *   k_cache, v_cache   [num_blocks][num_kv_heads][block_size][head_dim]
  *                      One (block, kv head) page of block_size*head_dim
