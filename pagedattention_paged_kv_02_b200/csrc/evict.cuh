@@ -10,7 +10,7 @@
 //
 // Two kernels. evict_select: one cluster of CTAs per (row, K/V head) finds
 // the kept positions (row_select.cuh), the order keys of its weights in shared
-// memory where they fit. evict_move: moves the rows.
+// memory where they fit. evict_move, a programmatic dependent: moves the rows.
 //
 // A destination block may be the row's own block at the same place (the cache
 // is then compacted in place) or a block no row reads. In place, the token
@@ -30,6 +30,7 @@
 // written once.
 #pragma once
 
+#include "decode.cuh"
 #include "row_select.cuh"
 
 namespace pa {
@@ -275,6 +276,9 @@ __global__ void __launch_bounds__(T)
         cut = cluster_cut<T, uint32_t>(cluster, sm.row, key_at, count, need);
         cluster_emit<T, uint32_t>(cluster, sm.row, key_at, count, cut, emit);
     }
+    // the move may be placed once every row is done; not before, or its waiting
+    // CTAs would be in the way of rows yet to start
+    allow_dependent_launch();
     cluster.sync();  // no CTA exits while another may read its shared memory
 }
 
@@ -298,6 +302,7 @@ __global__ void __launch_bounds__(T)
     const int h = blockIdx.y, b = blockIdx.z;
     const int n = evict_len(a, b, false);
     const int kept = min(n, a.budget);
+    wait_for_primary_grid();
     const int32_t *pos = a.kept + (size_t)((long long)b * a.H_kv + h) * a.budget;
 
     if ((int)blockIdx.x >= 2 * a.parts) {  // the weights

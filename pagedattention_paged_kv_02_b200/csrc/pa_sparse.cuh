@@ -597,10 +597,8 @@ pa_status pa_evict_tokens(void *k_cache, void *v_cache, float *weights_out,
                          (unsigned)num_seqs);
     // small CTAs, and more of them on an SM, where a CTA has little to move
     if ((long long)most * (a.row_bytes / 16) <= 1024)
-        evict_move_kernel<64, 4><<<move_grid, 64, 0, stream>>>(a);
-    else
-        evict_move_kernel<256, 8><<<move_grid, 256, 0, stream>>>(a);
-    return launch_status();
+        return launch_dependent(evict_move_kernel<64, 4>, move_grid, 64, 0, stream, a);
+    return launch_dependent(evict_move_kernel<256, 8>, move_grid, 256, 0, stream, a);
 }
 
 }  // extern "C"
