@@ -561,6 +561,9 @@ class PreparedOn(Prepared):
 
     def __init__(self, fn: str, tensors, args):
         super().__init__(fn, args)
+        # as C values, so that a call converts nothing (0.7 us of 2.5)
+        self._args = tuple(a if a is None or isinstance(a, ctypes.c_void_p) else kind(a)
+                           for a, kind in zip(self._args, self._fn.argtypes))
         self._tensors = [t for t in tensors if t is not None]
         devices = {t.device for t in self._tensors}
         if len(devices) != 1:
