@@ -416,7 +416,7 @@ PA_API pa_status pa_update_key_bounds(void *key_bounds, const void *k_cache,
  * largest score between them. Scores are compared in 64 bits; equal scores go
  * to the lower index, and a NaN score ranks above every number.
  *   selected     int32 [num_seqs][num_kv_heads][max_selected]
- *   max_selected > 0; num_first + num_last <= max_selected.
+ *   max_selected > 0, at most 2^30; num_first + num_last <= max_selected.
  *   max_context_len  host-side upper bound of context_lens, as in pa_decode.
  *   workspace    >= pa_select_blocks_workspace_size(...) bytes (8 per row, K/V
  *                head and block), 256-byte aligned; contents on entry are
@@ -443,7 +443,7 @@ PA_API pa_status pa_select_blocks(int32_t *selected, const void *q, const void *
  *                 past ceil(context_lens[b] / block_size), or a block id
  *                 outside the pool, is skipped and recorded as
  *                 PA_ERR_BAD_TABLE.
- *   max_selected  > 0
+ *   max_selected  > 0; max_selected * block_size at most 2^30
  *   partition_size  listed tokens per split (multiple of 16, <= 16384), a full
  *                 block_size counted for every entry; 0 = automatic; < 0 =
  *                 never split.
@@ -528,8 +528,8 @@ PA_API pa_status pa_decode_accumulate_weights(void *out, float *weights_out,
  *   weights_in, weights_out  fp32 [num_seqs][num_kv_heads][weights_stride],
  *                 weights_stride >= max_context_len; the same buffer, or
  *                 buffers that do not overlap.
- *   budget        > 0; num_first + num_last <= budget; the destination table
- *                 must hold min(budget, max_context_len) tokens.
+ *   budget        > 0, at most 2^30; num_first + num_last <= budget; the
+ *                 destination table must hold min(budget, max_context_len) tokens.
  *   max_context_len  host-side upper bound of context_lens, as in pa_decode; at
  *                 most 2^30.
  * new_context_lens and context_lens must not overlap. A token whose source or

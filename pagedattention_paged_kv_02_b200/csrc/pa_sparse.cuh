@@ -18,7 +18,9 @@ pa_status check_cache_shape(int num_seqs, int num_kv_heads, int head_dim, int bl
     return PA_OK;
 }
 
-constexpr int kMaxPositions = 1 << 30;  // of a row's weights: sums of positions stay in an int
+// Of a row's weights or listed tokens, and entries of its lists: sums of two stay
+// in an int.
+constexpr int kMaxPositions = 1 << 30;
 
 constexpr int kSelectStage = 24576;  // scores a selecting CTA keeps in shared memory, at most
 
@@ -59,10 +61,10 @@ int cluster_size(long long rows, long long items, int grain) {
 // per SM and a partition keeps more than 128 tokens (a partition's tokens are a
 // chain of 64 per step of its four warps: 1024 of them take about 20 us).
 int spread_partition(long long total, long long rows, int partition_size) {
-    if (total <= 0 || total > 0x7fffffffLL) return -1;
+    if (total <= 0 || total > kMaxPositions) return -1;
     if (partition_size > 0)
         return partition_size % kChunk != 0 || partition_size > kMaxPartition ? -1 : partition_size;
-    const int whole = round16((int)std::min(total, 1LL << 30));
+    const int whole = round16((int)total);
     if (partition_size < 0) return whole <= kMaxPartition ? whole : -1;
     int P = std::min(whole, 1024);
     while (rows * ((total + P - 1) / P) < 2 * 148 && P > 128) P = round16(P / 2);
@@ -263,6 +265,7 @@ pa_status pa_select_blocks(int32_t *selected, const void *q, const void *key_bou
     if (num_q_heads % num_kv_heads != 0) return PA_ERR_UNSUPPORTED;
     if ((long long)max_context_len > (long long)max_blocks_per_seq * block_size)
         return PA_ERR_INVALID_ARG;
+    if (max_selected > kMaxPositions) return PA_ERR_UNSUPPORTED;
     const long long blocks = ((long long)max_context_len + block_size - 1) / block_size;
     if (num_seqs == 0) return PA_OK;
     if (!selected || !q || !key_bounds || !block_tables || !context_lens)
@@ -387,6 +390,7 @@ pa_status pa_decode_selected_blocks(void *out, const void *q, const void *k_cach
     if (st != PA_OK) return st;
     if (num_q_heads <= 0 || max_selected <= 0 || !std::isfinite(scale)) return PA_ERR_INVALID_ARG;
     if (num_q_heads % num_kv_heads != 0) return PA_ERR_UNSUPPORTED;
+    if ((long long)max_selected * block_size > kMaxPositions) return PA_ERR_UNSUPPORTED;
     const int P = listed_partition(max_selected, block_size,
                                    listed_rows(num_seqs, num_q_heads, num_kv_heads),
                                    partition_size);
@@ -521,7 +525,7 @@ pa_status pa_evict_tokens(void *k_cache, void *v_cache, float *weights_out,
     if ((long long)max_context_len > (long long)max_blocks_per_seq * block_size ||
         std::min(budget, max_context_len) > (long long)dst_max_blocks_per_seq * block_size)
         return PA_ERR_INVALID_ARG;
-    if (max_context_len > kMaxPositions) return PA_ERR_UNSUPPORTED;
+    if (max_context_len > kMaxPositions || budget > kMaxPositions) return PA_ERR_UNSUPPORTED;
     if (num_seqs == 0) return PA_OK;
     if (!k_cache || !v_cache || !weights_out || !weights_in || !kept_positions ||
         !new_context_lens || !block_tables || !dst_block_tables || !context_lens)

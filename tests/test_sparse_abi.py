@@ -66,6 +66,7 @@ def test_select_blocks_host_checks(pa):
         (dict(max_ctx=129), pa.PA_ERR_INVALID_ARG), (dict(max_ctx=-1), pa.PA_ERR_INVALID_ARG),
         (dict(sel=ODD2), pa.PA_ERR_INVALID_ARG), (dict(q=None), pa.PA_ERR_INVALID_ARG),
         (dict(), pa.PA_ERR_WORKSPACE), (dict(ws_bytes=need - 1), pa.PA_ERR_WORKSPACE),
+        (dict(K=(1 << 30) + 1), pa.PA_ERR_UNSUPPORTED),
         (dict(ws=None, ws_bytes=need), pa.PA_ERR_WORKSPACE),
         (dict(ws=ctypes.c_void_p(0x10010), ws_bytes=need), pa.PA_ERR_WORKSPACE)])
 
@@ -88,6 +89,9 @@ def test_decode_selected_blocks_host_checks(pa):
         (dict(sel=ODD2), pa.PA_ERR_INVALID_ARG), (dict(out=ODD4), pa.PA_ERR_INVALID_ARG),
         (dict(part=24), pa.PA_ERR_INVALID_ARG), (dict(part=32768), pa.PA_ERR_INVALID_ARG),
         (dict(part=-1, K=1025), pa.PA_ERR_UNSUPPORTED), (dict(K=1 << 28), pa.PA_ERR_UNSUPPORTED),
+        # listed tokens past 2^30, whatever the partition
+        (dict(K=(1 << 26) + 1), pa.PA_ERR_UNSUPPORTED),
+        (dict(K=(1 << 26) + 1, part=16), pa.PA_ERR_UNSUPPORTED),
         (dict(part=16, K=9), pa.PA_ERR_WORKSPACE),
         (dict(part=16, K=9, ws=FAKE, ws_bytes=need - 1), pa.PA_ERR_WORKSPACE),
         (dict(part=16, K=9, ws=ctypes.c_void_p(0x10010), ws_bytes=need), pa.PA_ERR_WORKSPACE)])
@@ -127,6 +131,7 @@ def test_evict_tokens_host_checks(pa):
     refusals(pa, "pa_evict_tokens", args, cases + [
         (dict(budget=0), pa.PA_ERR_INVALID_ARG), (dict(first=60, last=5), pa.PA_ERR_INVALID_ARG),
         (dict(first=-1), pa.PA_ERR_INVALID_ARG),
+        (dict(budget=(1 << 30) + 1, dst_MB=8), pa.PA_ERR_UNSUPPORTED),
         (dict(first=2 ** 31 - 1, last=2 ** 31 - 1), pa.PA_ERR_INVALID_ARG),
         (dict(dst_MB=0), pa.PA_ERR_INVALID_ARG), (dict(dst_MB=3), pa.PA_ERR_INVALID_ARG),
         (dict(max_ctx=129, stride=200), pa.PA_ERR_INVALID_ARG),
