@@ -328,6 +328,27 @@ def test_special_weights(pa):
     assert kept[0, 0].tolist() == [i for i in range(64) if i != 30]
 
 
+@pytest.mark.parametrize("n", [2400, 9000])  # one CTA, a cluster
+@pytest.mark.parametrize("close", [127, 128, 129, 2047, 2049])
+def test_close_weights_around_the_cut(pa, n, close):
+    """As many weights within 2^-10 of each other as a selecting CTA ranks
+    directly, or sets aside, and one more or less; many of them equal, and the
+    cut at the first, in the middle and at the last of them."""
+    batch, _, _ = evict_case([n], 3, 64, 16, BF16, 16, 413)
+    g = torch.Generator().manual_seed(414 + close)
+    w = torch.full((1, 3, n), 2.0 ** -7)
+    at = torch.randperm(n, generator=g)
+    w[0, :, at[:close]] = 1 + torch.randint(0, 600, (3, close), generator=g) * 2.0 ** -20
+    w[0, :, at[close:close + 100]] = 64.0
+    for need in (1, close // 2, close - 1):
+        d = batch.to(DEV)
+        w_in = w.to(DEV)
+        dst = batch.block_tables
+        kept, lens = run_evict(pa, d, w_in, w_in, dst.to(DEV), 100 + need, 0, 0)
+        check_evict(batch, w, dst, 100 + need, 0, 0, d, w_in, w, kept, lens)
+    assert pa.pa_device_error() == 0
+
+
 def test_bad_ids_and_lengths_are_recorded(pa):
     batch, w, dst = evict_case([64, 40], 2, 64, 16, BF16, 32, 411)
     want = R.evict(w, batch.context_lens, 32, 0, 0)
