@@ -52,7 +52,13 @@
  *   key / value        [num_tokens][num_kv_heads][head_dim]
  *   Query head h reads K/V head h / (num_q_heads / num_kv_heads).
  *   q, out, key, value and the caches all have element type `dtype`;
- *   accumulation is fp32; bf16 outputs are rounded to nearest even.
+ *   accumulation is fp32; bf16 outputs are rounded to nearest even. Decode
+ *   over a bf16 cache, in every form, rounds the attention weights p to bf16
+ *   before they meet V (numerator and denominator take the same rounded
+ *   weights): at most 2^-7 sum p |V| of an output; the weights that
+ *   pa_decode_accumulate_weights returns are not rounded. Scores are fp32: a
+ *   q . K, or scale * q . K, beyond +-2.3e38 is outside their range, and a
+ *   row that has one may come out NaN.
  *
  * Conventions:
  *   - Every call is asynchronous on `stream`, never allocates device memory,
