@@ -47,9 +47,9 @@
 //     32-bit scores are within 2e of each other at the border by scores in 64
 //     bits.
 //   - Where that does not narrow them down (a score far out, equal blocks, an
-//     infinite or NaN score in the row), the border is found exactly
-//     (row_select.cuh), and all blocks within 2e of it are scored and
-//     selected in 64 bits.
+//     infinite or NaN score in the row, one within 2e of the largest number),
+//     the border is found exactly (row_select.cuh), and all blocks within 2e of
+//     it are scored and selected in 64 bits.
 //
 // Scoring and selecting in one kernel (a cluster of CTAs per row, scores in
 // shared memory, no workspace) was built first and measured slower: 123 us on
@@ -338,9 +338,14 @@ __device__ __forceinline__ bool select_by_bins(const SelectArgs &a, SelectSmem &
     bins.err = __uint_as_float(sm.err);
     if (sm.lo > sm.hi || !(bins.err < INFINITY)) return false;
     bins.lo = key_value(sm.lo);
-    const float width = key_value(sm.hi) - bins.lo;
+    const float top = key_value(sm.hi), width = top - bins.lo;
     bins.scale = width > 0.f ? (float)kBins / width : 0.f;
     if (!(width < INFINITY) || !(bins.scale < INFINITY)) return false;
+    // a score less or plus 2e must not leave the range: equal scores have a scale
+    // of 0, and 0 times an infinity no bin
+    if (!(__fsub_rd(bins.lo, 2.f * bins.err) > -INFINITY) ||
+        !(__fadd_ru(top, 2.f * bins.err) < INFINITY))
+        return false;
 
     for (int i = tid; i < count; i += THREADS) {
         const uint32_t k = (uint32_t)(keys[i] >> 32);
@@ -526,7 +531,9 @@ __global__ void __launch_bounds__(THREADS)
     __syncthreads();
     const T *q = reinterpret_cast<const T *>(a.q) + ((size_t)b * a.H_q + (size_t)h * a.group) * D;
     const int32_t *table = a.block_tables + (size_t)b * a.MB + a.first;
-    auto emit = [&](int place, int i) { dst[a.first + place] = a.first + i; };
+    auto emit = [&](int place, int i) {  // (never past the places between first and last)
+        if (place < c.need) dst[a.first + place] = a.first + i;
+    };
     if (!select_by_bins<THREADS, D, T>(a, sm, q, table, h, count, (uint32_t)c.need, keys, emit)) {
         const Cut<uint64_t> cut =
             exact_cut<THREADS, D, T>(a, sm, q, table, h, count, (uint32_t)c.need, keys);
