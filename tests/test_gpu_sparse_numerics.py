@@ -93,3 +93,77 @@ def test_outputs_element_by_element(pa, shape):
         err = (out.cpu().double() - exact).abs()
         assert bool((err <= off).all()), (name, (err / off).max().item())
     assert pa.pa_device_error() == 0
+
+
+# ---------------------------------------------------------------- block scores
+def score_inputs(kind, dtype, D, group, seed):
+    """q [B, H_q, D], bounds [NB, H, 2, D] and tables whose scores have terms of
+    the given kind."""
+    g = torch.Generator().manual_seed(seed)
+    B, H, n = 2, 2, 700
+    NB = B * n
+    rand = lambda *s: torch.randn(*s, generator=g)
+    q, bounds = rand(B, H * group, D), rand(NB, H, 2, D)
+    if kind == "cancelling":         # pairs of large terms that leave a small sum
+        q = q.abs() + 0.5
+        q[..., 1::2] = q[..., ::2]
+        bounds *= 2.0 ** -9
+        big = 2.0 ** torch.randint(0, 12, (NB, H, 1, D // 2), generator=g).float()
+        bounds[..., ::2] += big
+        bounds[..., 1::2] -= big
+    elif kind == "wide":             # exponents over 2^-60 .. 2^60 in one sum
+        q *= 2.0 ** torch.randint(-30, 31, q.shape, generator=g).float()
+        bounds *= 2.0 ** torch.randint(-30, 31, bounds.shape, generator=g).float()
+    elif kind == "cut":              # few large terms, the rest just at what a sum keeps beside them
+        q[:] = 1.0
+        small = 1.0 + torch.rand(NB, H, 2, D, generator=g)
+        bounds = small * 2.0 ** torch.randint(-26, -20, bounds.shape, generator=g).float()
+        bounds[..., ::16] = 1.0 + torch.rand(NB, H, 2, D // 16, generator=g)
+        bounds[NB // 2:, ..., 16:32] *= -1.0
+    elif kind == "tiny":             # products below the smallest number of 32 bits
+        q *= 2.0 ** -70
+        bounds *= 2.0 ** torch.randint(-80, -60, bounds.shape, generator=g).float()
+    elif kind == "large":            # sums near the end of the range
+        q *= 2.0 ** 60
+        bounds *= 2.0 ** 59
+    tables = torch.randperm(NB, generator=g).reshape(B, n).int()
+    return q.to(dtype), bounds.to(dtype), tables
+
+
+@pytest.mark.parametrize("kind", ["normal", "cancelling", "wide", "cut", "tiny", "large"])
+@pytest.mark.parametrize("group", [1, 5, 16])
+@pytest.mark.parametrize("dtype,D", [(BF16, 64), (BF16, 128), (F32, 64), (F32, 128)])
+def test_scores_are_within_their_error_bounds(pa, dtype, D, group, kind):
+    """The workspace holds a 32-bit score and its error bound for every contested
+    block; the 64-bit score lies within. (The 64-bit one is itself off by less
+    than 2 D * 2^-53 of its terms' sum, 2^-28 of the least bound here.)"""
+    bs, count, first, last = 16, 30, 2, 1
+    q, bounds, tables = score_inputs(kind, dtype, D, group, 620 + group)
+    B, n = tables.shape
+    H = bounds.shape[1]
+    lens = torch.full((B,), n * bs, dtype=torch.int32)
+    size = pa.pa_select_blocks_workspace_size(B, H, bs, n * bs)
+    ws = torch.zeros(size, dtype=torch.uint8, device=DEV)
+    sel = torch.empty(B, H, count, dtype=torch.int32, device=DEV)
+    pa.pa_select_blocks(sel, q.to(DEV), bounds.to(DEV), tables.to(DEV), lens.to(DEV), n * bs, bs,
+                        first, last, ws)
+    torch.cuda.synchronize()
+    middle = n - first - last
+    entry = ws.cpu().view(torch.int64).view(B, H, n)[..., :middle]
+    key = (entry >> 32) & 0xffffffff
+    pattern = torch.where(key >= 1 << 31, key & 0x7fffffff, key ^ 0xffffffff)
+    low = lambda x: torch.where(x >= 1 << 31, x - (1 << 32), x).int().view(torch.float32).double()
+    score, off = low(pattern), low(entry & 0xffffffff)
+    exact = torch.stack([torch.stack([R.block_scores(q[b], bounds, tables[b], n, h, group)
+                                      for h in range(H)]) for b in range(B)])
+    exact = exact[..., first:n - last]
+    bounded = torch.isfinite(off)
+    assert bool(bounded.all()) or kind == "large"
+    assert int(bounded.sum()) > 0
+    ratio = ((score - exact).abs() / off)[bounded].max().item()
+    print(f"{kind} {dtype} D {D} group {group}: {ratio:.3f} of the bound")
+    assert ratio <= 1.0
+    # and what is selected by them is the 64-bit choice
+    want = R.select_blocks(q, bounds, tables, lens, bs, count, first, last)
+    assert torch.equal(sel.cpu(), want)
+    assert pa.pa_device_error() == 0
