@@ -587,6 +587,48 @@ class PreparedOn(Prepared):
             raise PAError(self.name, st)
 
 
+class PreparedWithWorkspace(PreparedOn):
+    """A prepared call that provides its workspace, whose pointer is argument
+    ``at``. The allocator orders memory by the stream it was asked for on, so a
+    workspace is allocated on the stream that the kernels run on: memory freed
+    there is not in use elsewhere, and what this call gives back is handed out
+    there only. Streams may overlap, so each has one; a captured launch gets one
+    from the graph's own memory, which lasts as long as the graph."""
+
+    def __init__(self, fn: str, tensors, args, at: int, nbytes: int):
+        super().__init__(fn, tensors, args)
+        self._at, self._nbytes = at, nbytes
+        self._on_stream = {}  # stream handle -> its workspace, arguments
+
+    def _allocate(self):
+        ws = torch.empty(self._nbytes, dtype=torch.uint8, device=f"cuda:{self._device}")
+        return ws, self._args[:self._at] + (_p(ws),) + self._args[self._at + 1:]
+
+    def __call__(self, stream=None):
+        if stream is not None and stream.device_index != self._device:
+            raise ValueError(f"{self.name}: the stream is on another device than the tensors")
+        here = torch.cuda.current_device() == self._device
+        if here and stream is not None:
+            here = stream.cuda_stream == torch._C._cuda_getCurrentRawStream(self._device)
+        if here:
+            return self._launch()
+        # the allocator and the state of a capture go by the current stream
+        with torch.cuda.stream(torch.cuda.current_stream(self._device) if stream is None else stream):
+            return self._launch()
+
+    def _launch(self):
+        handle = torch._C._cuda_getCurrentRawStream(self._device)
+        if torch._C._cuda_isCurrentStreamCapturing():
+            kept = self._allocate()
+        else:
+            kept = self._on_stream.get(handle)
+            if kept is None:
+                kept = self._on_stream[handle] = self._allocate()
+        st = self._fn(*kept[1], handle)
+        if st != PA_OK:
+            raise PAError(self.name, st)
+
+
 def _rows(block_tables, lens, what):
     """Number of rows and table width of int32 ``block_tables`` [rows, MB]; every
     tensor of ``lens`` is int32 [rows]."""
@@ -642,8 +684,9 @@ def prepare_select_blocks(selected, q, key_bounds, block_tables, context_lens,
                           num_last: int = 0,
                           workspace: Optional[torch.Tensor] = None) -> Prepared:
     """``pa_select_blocks`` with its arguments marshalled once. Without a
-    ``workspace`` the prepared call gets one of its own (so, like any prepared
-    call with a workspace, it must not overlap itself on two streams)."""
+    ``workspace`` the prepared call has one of its own for each stream it is
+    called on and for each capture. (Calls that overlap write the same
+    ``selected`` all the same.)"""
     _check_int(selected, torch.int32, "selected")
     B, MB = _rows(block_tables, (context_lens,), ("context_lens",))
     NB, H_kv, D = _bounds_shape(key_bounds)
@@ -653,17 +696,16 @@ def prepare_select_blocks(selected, q, key_bounds, block_tables, context_lens,
         raise ValueError("selected must be [num_seqs, num_kv_heads, max_selected]")
     if q.dtype != key_bounds.dtype:
         raise TypeError("q and key_bounds must share one dtype")
-    if workspace is None:
-        n = pa_select_blocks_workspace_size(B, H_kv, block_size, max_context_len)
-        workspace = torch.empty(n, dtype=torch.uint8, device=q.device)
-    call = PreparedOn("pa_select_blocks",
-                      (selected, q, key_bounds, block_tables, context_lens, workspace),
-                      (_p(selected), _p(q), _p(key_bounds), _p(block_tables), _p(context_lens),
-                       selected.shape[2], int(num_first), int(num_last), B, q.shape[1], H_kv, D,
-                       int(block_size), NB, MB, int(max_context_len), _p(workspace),
-                       _nbytes(workspace), _dt(q)))
-    call.workspace = workspace
-    return call
+    tensors = (selected, q, key_bounds, block_tables, context_lens)
+    head = (_p(selected), _p(q), _p(key_bounds), _p(block_tables), _p(context_lens),
+            selected.shape[2], int(num_first), int(num_last), B, q.shape[1], H_kv, D,
+            int(block_size), NB, MB, int(max_context_len))
+    if workspace is not None:
+        return PreparedOn("pa_select_blocks", tensors + (workspace,),
+                          head + (_p(workspace), _nbytes(workspace), _dt(q)))
+    n = pa_select_blocks_workspace_size(B, H_kv, block_size, max_context_len)
+    return PreparedWithWorkspace("pa_select_blocks", tensors, head + (None, n, _dt(q)),
+                                 len(head), n)
 
 
 def pa_select_blocks(selected, q, key_bounds, block_tables, context_lens, max_context_len: int,
@@ -675,11 +717,8 @@ def pa_select_blocks(selected, q, key_bounds, block_tables, context_lens, max_co
     order, -1 past the last. ``workspace``: at least
     :func:`pa_select_blocks_workspace_size` bytes, allocated for the call when
     None."""
-    call = prepare_select_blocks(selected, q, key_bounds, block_tables, context_lens,
-                                 max_context_len, block_size, num_first, num_last, workspace)
-    call(stream)
-    if workspace is None and stream is not None:
-        call.workspace.record_stream(stream)
+    prepare_select_blocks(selected, q, key_bounds, block_tables, context_lens, max_context_len,
+                          block_size, num_first, num_last, workspace)(stream)
 
 
 def pa_decode_selected_blocks_workspace_size(num_seqs: int, num_q_heads: int, num_kv_heads: int,
