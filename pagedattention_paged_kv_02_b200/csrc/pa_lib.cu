@@ -66,20 +66,32 @@ EncodeTiledFn encode_fn() {
     return fn;
 }
 
+// The encoding needs a context that is current in the calling thread, and unlike
+// the runtime's calls the driver's do not make the device's current: in a host
+// thread that has made no other CUDA call yet, cudaSetDevice does.
+template <typename... A>
+bool encode_tiled(CUtensorMap *m, A... args) {
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return false;
+    if (fn(m, args...) == CUDA_SUCCESS) return true;
+    int dev = -1;
+    return cudaGetDevice(&dev) == cudaSuccess && cudaSetDevice(dev) == cudaSuccess &&
+           fn(m, args...) == CUDA_SUCCESS;
+}
+
 // A 4-D view [num_blocks][H_kv][bs][D] of a bf16 cache with a box of
 // box_rows tokens x 64 dims (128 bytes) and 128-byte swizzle.
 bool encode_cache_map(CUtensorMap *m, const void *cache, int NB, int H_kv, int bs, int D,
                       int box_rows) {
-    EncodeTiledFn fn = encode_fn();
-    if (!fn) return false;
     cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)bs, (cuuint64_t)H_kv, (cuuint64_t)NB};
     cuuint64_t strides[3] = {(cuuint64_t)D * 2, (cuuint64_t)bs * D * 2,
                              (cuuint64_t)H_kv * bs * D * 2};
     cuuint32_t box[4] = {64, (cuuint32_t)box_rows, 1, 1};
     cuuint32_t estr[4] = {1, 1, 1, 1};
-    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(cache), dims, strides, box,
-              estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    return encode_tiled(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4u, const_cast<void *>(cache), dims,
+                        strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                        CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
 }
 
 // KV tokens per partition, or -1 if the request cannot be met.
@@ -187,15 +199,14 @@ pa_status launch_prefill_tc(const PrefillArgs &a, const CUtensorMap &mq, const C
 // A 4-D view [num_blocks][H_kv][bs][128] of a one-byte (E4M3) cache with a
 // box of 16 tokens x 128 dims (128 bytes) and 128-byte swizzle.
 bool encode_cache_map_u8(CUtensorMap *m, const void *cache, int NB, int H_kv, int bs) {
-    EncodeTiledFn fn = encode_fn();
-    if (!fn) return false;
     cuuint64_t dims[4] = {128, (cuuint64_t)bs, (cuuint64_t)H_kv, (cuuint64_t)NB};
     cuuint64_t strides[3] = {128, (cuuint64_t)bs * 128, (cuuint64_t)H_kv * bs * 128};
     cuuint32_t box[4] = {128, (cuuint32_t)kChunk, 1, 1};
     cuuint32_t estr[4] = {1, 1, 1, 1};
-    return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void *>(cache), dims, strides, box,
-              estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    return encode_tiled(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4u, const_cast<void *>(cache), dims,
+                        strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                        CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
 }
 
 template <int NW, int NS, int CT, bool INT8>
@@ -702,8 +713,6 @@ static pa_status prefill_impl(void *out, const void *q, const void *k_cache, con
     const long long qtiles = (max_query_len + cta_rows - 1) / cta_rows;
     if (qtiles > 65535 || num_chunks > 65535) return PA_ERR_UNSUPPORTED;
 
-    EncodeTiledFn fn = encode_fn();
-    if (!fn) return PA_ERR_CUDA;
     CUtensorMap mq, mk, mv;
     {
         cuuint64_t dims[3] = {(cuuint64_t)head_dim, (cuuint64_t)num_q_heads,
@@ -712,9 +721,10 @@ static pa_status prefill_impl(void *out, const void *q, const void *k_cache, con
                                  (cuuint64_t)num_q_heads * head_dim * 2};
         cuuint32_t box[3] = {64, 1, kPfRows};
         cuuint32_t estr[3] = {1, 1, 1};
-        if (fn(&mq, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(q), dims, strides, box,
-               estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+        if (!encode_tiled(&mq, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3u, const_cast<void *>(q), dims,
+                          strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                          CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE))
             return PA_ERR_CUDA;
     }
     if (!encode_cache_map(&mk, k_cache, num_blocks, num_kv_heads, block_size, head_dim, 16) ||
