@@ -114,10 +114,20 @@ size_t workspace_bytes(int B, int H_q, int D, int max_ctx, int P) {
     return (o + 255) / 256 * 256 + (l + 255) / 256 * 256;
 }
 
+// Lets launches of `kernel` have up to `most` bytes of dynamic shared memory.
+// The limit belongs to the kernel, not to a launch: with one thread's smaller
+// limit set between another's limit and its launch, that launch would be refused.
+// So it is the same for every call, the most that any launch of the kernel has;
+// a launch's own size decides what it occupies.
 template <typename K>
-cudaError_t set_smem(K kernel, size_t bytes) {
-    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+cudaError_t allow_smem(K kernel, size_t most) {
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
 }
+
+// Bytes of a split CTA's table slice -- block ids, and for listed blocks their
+// numbers of valid tokens -- and the most it has: blocks of 16 tokens.
+size_t slice_bytes(int P, int bs, int arrays = 1) { return ((size_t)P / bs + 2) * 4 * arrays; }
+constexpr size_t kMaxSlice = ((size_t)kMaxPartition / 16 + 2) * 4;
 
 // ------------------------------------------------------------- decode
 // Launch shapes (measured on B200 in sweeps of warps x stages): the bf16
@@ -150,21 +160,18 @@ pa_status launch_clusters(K kernel, dim3 grid, int threads, int cs, size_t smem,
     return launch_status();
 }
 
-// Bytes of a split CTA's table slice: block ids, and for listed blocks their
-// numbers of valid tokens.
-template <Span SPAN>
-size_t slice_bytes(const DecodeArgs &a) {
-    return ((size_t)a.P / a.bs + 2) * 4 * (SPAN == Span::kListed ? 2 : 1);
-}
+// Arrays of a table slice.
+constexpr int slice_arrays(Span span) { return span == Span::kListed ? 2 : 1; }
 
 template <int D, int NW, int NS, Span SPAN = Span::kOwn>
 pa_status launch_decode_bf16(const DecodeArgs &a, const CUtensorMap &mk, const CUtensorMap &mv,
                              dim3 grid, cudaStream_t st) {
     constexpr int STAGE = 2 * kChunk * D * 2;
     using L = DecodeSmem<NW, NS, STAGE, kHeadsBf16, D>;
-    const size_t smem = 1024 + L::kTable + slice_bytes<SPAN>(a);
+    constexpr size_t fixed = 1024 + L::kTable;
+    const size_t smem = fixed + slice_bytes(a.P, a.bs, slice_arrays(SPAN));
     auto k = decode_split_bf16<D, NW, NS, SPAN>;
-    if (set_smem(k, smem) != cudaSuccess) return PA_ERR_CUDA;
+    if (allow_smem(k, fixed + kMaxSlice * slice_arrays(SPAN)) != cudaSuccess) return PA_ERR_CUDA;
     if (a.cluster) return launch_clusters(k, grid, NW * 32, (int)grid.x, smem, st, a, mk, mv);
     k<<<grid, NW * 32, smem, st>>>(a, mk, mv);
     return launch_status();
@@ -174,9 +181,10 @@ template <int D, int NW, int NS>
 pa_status launch_decode_f32(const DecodeArgs &a, dim3 grid, cudaStream_t st) {
     constexpr int STAGE = 2 * kChunk * D * 4;
     using L = DecodeSmem<NW, NS, STAGE, kHeadsF32, D>;
-    const size_t smem = 1024 + L::kTable + slice_bytes<Span::kOwn>(a);
+    constexpr size_t fixed = 1024 + L::kTable;
+    const size_t smem = fixed + slice_bytes(a.P, a.bs);
     auto k = decode_split_f32<D, NW, NS>;
-    if (set_smem(k, smem) != cudaSuccess) return PA_ERR_CUDA;
+    if (allow_smem(k, fixed + kMaxSlice) != cudaSuccess) return PA_ERR_CUDA;
     k<<<grid, NW * 32, smem, st>>>(a);
     return launch_status();
 }
@@ -186,7 +194,7 @@ pa_status launch_prefill_tc(const PrefillArgs &a, const CUtensorMap &mq, const C
                             const CUtensorMap &mv, dim3 grid, cudaStream_t st) {
     const size_t smem = 1024 + pf_smem_bytes(D);
     auto k = prefill_tc_kernel<D, WIN>;
-    if (set_smem(k, smem) != cudaSuccess) return PA_ERR_CUDA;
+    if (allow_smem(k, smem) != cudaSuccess) return PA_ERR_CUDA;
     // the kernel's register split must fit the registers it launches with,
     // or the warpgroups that grow would wait forever
     cudaFuncAttributes fa;
@@ -214,9 +222,10 @@ pa_status launch_decode_q8(const DecodeArgs &a, const CUtensorMap &mk, const CUt
                              dim3 grid, cudaStream_t st) {
     constexpr int STAGE = 2 * CT * 128;
     using L = DecodeSmem<NW, NS, STAGE, kHeadsBf16, 128>;
-    const size_t smem = 1024 + L::kTable + ((size_t)a.P / a.bs + 2) * 4;
+    constexpr size_t fixed = 1024 + L::kTable;
+    const size_t smem = fixed + slice_bytes(a.P, a.bs);
     auto k = decode_split_q8<NW, NS, CT, INT8>;
-    if (set_smem(k, smem) != cudaSuccess) return PA_ERR_CUDA;
+    if (allow_smem(k, fixed + kMaxSlice) != cudaSuccess) return PA_ERR_CUDA;
     k<<<grid, NW * 32, smem, st>>>(a, mk, mv);
     return launch_status();
 }
@@ -298,9 +307,10 @@ template <int D, int MT>
 pa_status launch_prefix(const DecodeArgs &a, const CUtensorMap &mk, const CUtensorMap &mv,
                         dim3 grid, cudaStream_t st) {
     using L = PrefixSmem<D, MT>;
-    const size_t smem = 1024 + L::kTable + ((size_t)a.P_prefix / a.bs + 2) * 4;
+    constexpr size_t fixed = 1024 + L::kTable;
+    const size_t smem = fixed + slice_bytes(a.P_prefix, a.bs);
     auto k = decode_prefix_bf16<D, MT>;
-    if (set_smem(k, smem) != cudaSuccess) return PA_ERR_CUDA;
+    if (allow_smem(k, fixed + kMaxSlice) != cudaSuccess) return PA_ERR_CUDA;
     k<<<grid, kPrefixWarps * 32, smem, st>>>(a, mk, mv);
     return launch_status();
 }
@@ -312,9 +322,10 @@ pa_status launch_tail(const DecodeArgs &a, const CUtensorMap &mk, const CUtensor
                       bool dependent, cudaStream_t st) {
     constexpr int STAGE = 2 * kChunk * D * 2;
     using L = DecodeSmem<kDecodeWarps, kDecodeStages, STAGE, kHeadsBf16, D>;
-    const size_t smem = 1024 + L::kTable + ((size_t)a.P / a.bs + 2) * 4;
+    constexpr size_t fixed = 1024 + L::kTable;
+    const size_t smem = fixed + slice_bytes(a.P, a.bs);
     auto k = decode_split_bf16<D, kDecodeWarps, kDecodeStages, Span::kTail>;
-    if (set_smem(k, smem) != cudaSuccess) return PA_ERR_CUDA;
+    if (allow_smem(k, fixed + kMaxSlice) != cudaSuccess) return PA_ERR_CUDA;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -25,6 +25,7 @@ constexpr int kMaxPositions = 1 << 30;
 constexpr int kSelectStage = 24576;  // scores a selecting CTA keeps in shared memory, at most
 
 constexpr int kEvictStage = 40960;   // weights a selecting CTA keeps in shared memory, at most
+constexpr size_t evict_stage_bytes(int weights) { return ((size_t)weights + 8) * 4; }
 
 // A programmatic dependent of the launch before it: its CTAs may be placed
 // while that grid finishes, and wait for it before they use its results.
@@ -146,9 +147,10 @@ void fill_decode(DecodeArgs &a, const DecodeShape &s, void *out, const void *q,
 
 template <int D, int HT, Span SPAN>
 pa_status launch_rows_f32_tile(const DecodeArgs &a, dim3 grid, cudaStream_t st) {
-    const size_t smem = 1024 + F32Smem<D, HT>::kTable + slice_bytes<SPAN>(a);
+    constexpr size_t fixed = 1024 + F32Smem<D, HT>::kTable;
+    const size_t smem = fixed + slice_bytes(a.P, a.bs, slice_arrays(SPAN));
     auto k = decode_rows_f32<D, HT, SPAN>;
-    if (set_smem(k, smem) != cudaSuccess) return PA_ERR_CUDA;
+    if (allow_smem(k, fixed + kMaxSlice * slice_arrays(SPAN)) != cudaSuccess) return PA_ERR_CUDA;
     if (a.cluster) return launch_clusters(k, grid, kF32Warps * 32, (int)grid.x, smem, st, a);
     k<<<grid, kF32Warps * 32, smem, st>>>(a);
     return launch_status();
@@ -329,7 +331,7 @@ pa_status pa_select_blocks(int32_t *selected, const void *q, const void *key_bou
     auto launch = [&](auto kernel, int threads) {
         const dim3 grid((unsigned)num_kv_heads, (unsigned)num_seqs);
         const size_t smem = (size_t)a.stage * sizeof(uint64_t);
-        if (set_smem(kernel, smem) != cudaSuccess) return PA_ERR_CUDA;
+        if (allow_smem(kernel, kSelectStage * sizeof(uint64_t)) != cudaSuccess) return PA_ERR_CUDA;
         if (contested) return launch_dependent(kernel, grid, threads, smem, stream, a);
         // without the scoring kernel in between, the launch before may still
         // read what this one writes
@@ -567,20 +569,22 @@ pa_status pa_evict_tokens(void *k_cache, void *v_cache, float *weights_out,
     const int cs = cluster_size(rows, max_context_len, 4096);
     a.stage = std::min((max_context_len + cs - 1) / cs, kEvictStage);
     const dim3 grid((unsigned)cs, (unsigned)num_kv_heads, (unsigned)num_seqs);
-    const size_t smem = ((size_t)a.stage + 8) * 4;
+    const size_t smem = evict_stage_bytes(a.stage), limit = evict_stage_bytes(kEvictStage);
     // a row to a CTA of its own where there are rows enough, or they are short
     pa_status r = PA_OK;
     if (cs > 1) {
-        if (set_smem(evict_select_kernel<512, CtaCluster>, smem) != cudaSuccess)
-            return PA_ERR_CUDA;
-        r = launch_clusters(evict_select_kernel<512, CtaCluster>, grid, 512, cs, smem, stream, a);
+        auto k = evict_select_kernel<512, CtaCluster>;
+        if (allow_smem(k, limit) != cudaSuccess) return PA_ERR_CUDA;
+        r = launch_clusters(k, grid, 512, cs, smem, stream, a);
     } else if (max_context_len > 16384) {
-        if (set_smem(evict_select_kernel<512, OneCta>, smem) != cudaSuccess) return PA_ERR_CUDA;
-        evict_select_kernel<512, OneCta><<<grid, 512, smem, stream>>>(a);
+        auto k = evict_select_kernel<512, OneCta>;
+        if (allow_smem(k, limit) != cudaSuccess) return PA_ERR_CUDA;
+        k<<<grid, 512, smem, stream>>>(a);
         r = launch_status();
     } else {
-        if (set_smem(evict_select_kernel<256, OneCta>, smem) != cudaSuccess) return PA_ERR_CUDA;
-        evict_select_kernel<256, OneCta><<<grid, 256, smem, stream>>>(a);
+        auto k = evict_select_kernel<256, OneCta>;
+        if (allow_smem(k, limit) != cudaSuccess) return PA_ERR_CUDA;
+        k<<<grid, 256, smem, stream>>>(a);
         r = launch_status();
     }
     if (r != PA_OK) return r;
