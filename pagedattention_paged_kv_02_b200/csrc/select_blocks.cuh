@@ -389,6 +389,10 @@ __device__ __forceinline__ bool select_by_bins(const SelectArgs &a, SelectSmem &
     above = __reduce_add_sync(0xffffffffu, above);
     if (lane == 0) atomicAdd(&sm.above, above);
     __syncthreads();
+    // fewer than `need` blocks lie above the border's bin; had more been marked,
+    // they would not fit the list (a test of each place as it is written instead:
+    // 27.5 against 26.7 us for 128 ragged rows of up to 256 blocks and 8 heads)
+    if (sm.above >= need) return false;
     const uint32_t zone = sm.zone, places = need - sm.above;
     uint32_t least = 1;  // the mark of a block that is in
     if (zone != places) {
@@ -531,9 +535,7 @@ __global__ void __launch_bounds__(THREADS)
     __syncthreads();
     const T *q = reinterpret_cast<const T *>(a.q) + ((size_t)b * a.H_q + (size_t)h * a.group) * D;
     const int32_t *table = a.block_tables + (size_t)b * a.MB + a.first;
-    auto emit = [&](int place, int i) {  // (never past the places between first and last)
-        if (place < c.need) dst[a.first + place] = a.first + i;
-    };
+    auto emit = [&](int place, int i) { dst[a.first + place] = a.first + i; };
     if (!select_by_bins<THREADS, D, T>(a, sm, q, table, h, count, (uint32_t)c.need, keys, emit)) {
         const Cut<uint64_t> cut =
             exact_cut<THREADS, D, T>(a, sm, q, table, h, count, (uint32_t)c.need, keys);
