@@ -618,7 +618,8 @@ class PreparedWithWorkspace(PreparedOn):
 
     def _launch(self):
         handle = torch._C._cuda_getCurrentRawStream(self._device)
-        if torch._C._cuda_isCurrentStreamCapturing():
+        # (stream 0 cannot be captured; asking costs 1 us)
+        if handle != 0 and torch._C._cuda_isCurrentStreamCapturing():
             kept = self._allocate()
         else:
             kept = self._on_stream.get(handle)
