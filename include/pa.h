@@ -58,7 +58,9 @@
  *   weights): at most 2^-7 sum p |V| of an output; the weights that
  *   pa_decode_accumulate_weights returns are not rounded. Scores are fp32: a
  *   q . K, or scale * q . K, beyond +-2.3e38 is outside their range, and a
- *   row that has one may come out NaN.
+ *   row that has one may come out NaN. A NaN in a row's query or in a key that
+ *   it attends makes the row (of that query head) NaN; keys and values that
+ *   are not attended are never used, whatever they hold.
  *
  * Conventions:
  *   - Every call is asynchronous on `stream`, never allocates device memory,

@@ -185,6 +185,9 @@ struct DecodeSmem {
 
 // Cross-warp merge of per-warp online-softmax states and the final write:
 // the output (one partition) or the partition's normalised partial and lse.
+// A NaN score leaves the maxima (fmaxf passes over it) and makes its warp's sum
+// NaN. That sum, the partition's lse and the merges hand it on, so that the
+// row's output is NaN; only a sum of 0 means that nothing was attended.
 template <int D, int NW, int HT, typename OutT>
 __device__ __forceinline__ void decode_epilogue(const DecodeArgs &a, const float *red_o,
                                                 const float *red_m, const float *red_l, int b,
@@ -206,8 +209,11 @@ __device__ __forceinline__ void decode_epilogue(const DecodeArgs &a, const float
                 o0 += f * red_o[(w * HT + row) * OS + d];
                 o1 += f * red_o[(w * HT + row) * OS + d + 1];
             }
+        } else {  // no usable token: the sums are 0; scores all NaN: they are NaN
+#pragma unroll
+            for (int w = 0; w < NW; ++w) L += red_l[w * HT + row];
         }
-        const float inv = L > 0.f ? oscale / L : 0.f;
+        const float inv = L == 0.f ? 0.f : oscale / L;
         const size_t bh = (size_t)b * a.H_q + h0 + row;
         if (n_splits <= 1) {
             if constexpr (sizeof(OutT) == 2) {
@@ -220,7 +226,7 @@ __device__ __forceinline__ void decode_epilogue(const DecodeArgs &a, const float
         } else {
             *reinterpret_cast<float2 *>(a.part_o + (bh * a.S_max + s) * D + d) =
                 make_float2(o0 * inv, o1 * inv);
-            if (d == 0) a.part_lse[bh * a.S_max + s] = L > 0.f ? M + log2f(L) : -INFINITY;
+            if (d == 0) a.part_lse[bh * a.S_max + s] = L == 0.f ? -INFINITY : M + log2f(L);
         }
     }
 }
@@ -275,6 +281,9 @@ __device__ __forceinline__ void cluster_epilogue(const DecodeArgs &a, const floa
                 L += f * red_l[w * HT + row];
                 o += f * red_o[(w * HT + row) * OS + d];
             }
+        } else {
+#pragma unroll
+            for (int w = 0; w < NW; ++w) L += red_l[w * HT + row];
         }
         own_o[idx] = o;
         if (d == 0) {
@@ -297,9 +306,11 @@ __device__ __forceinline__ void cluster_epilogue(const DecodeArgs &a, const floa
                 L += f * *cluster.map_shared_rank(own_l + row, r);
                 o += f * *cluster.map_shared_rank(own_o + idx, r);
             }
+        } else {
+            for (int r = 0; r < ranks; ++r) L += *cluster.map_shared_rank(own_l + row, r);
         }
         reinterpret_cast<OutT *>(a.out)[((size_t)b * a.H_q + h0) * D + idx] =
-            OutT(L > 0.f ? o / L : 0.f);
+            OutT(L == 0.f ? 0.f : o / L);
     }
     cluster.sync();  // no CTA exits while another may read its shared memory
 }
@@ -340,23 +351,28 @@ __device__ __forceinline__ void write_weights(const DecodeArgs &a, int b, int kv
     }
 }
 
-// kWeighted: the maximum and the sum of weights of a partition's rows; with
-// weights_here the CTA has every score of its K/V head and finishes the weights.
+// kWeighted: the maximum and the sum of weights of a row over the CTA's warps.
+template <int NW, int HT>
+__device__ __forceinline__ void row_statistics(const float *red_m, const float *red_u, int row,
+                                               float &M, float &U) {
+    M = -INFINITY;
+    U = 0.f;
+#pragma unroll
+    for (int w = 0; w < NW; ++w) M = fmaxf(M, red_m[w * HT + row]);
+#pragma unroll
+    for (int w = 0; w < NW; ++w)  // without a maximum: 0, or NaN for NaN scores
+        U += M == -INFINITY ? red_u[w * HT + row]
+                            : exp2f(red_m[w * HT + row] - M) * red_u[w * HT + row];
+}
+
+// kWeighted: the statistics of a partition's rows; with weights_here the CTA has
+// every score of its K/V head and finishes the weights.
 template <int NW, int HT>
 __device__ __forceinline__ void write_statistics(const DecodeArgs &a, float *red_m, float *red_u,
                                                  int b, int h0, int nh, int s, int kvh, int ctx) {
     if (a.weights_here) {
         float M = -INFINITY, U = 0.f;
-        if (threadIdx.x < nh) {
-            const int row = threadIdx.x;
-#pragma unroll
-            for (int w = 0; w < NW; ++w) M = fmaxf(M, red_m[w * HT + row]);
-            if (M != -INFINITY) {
-#pragma unroll
-                for (int w = 0; w < NW; ++w)
-                    U += exp2f(red_m[w * HT + row] - M) * red_u[w * HT + row];
-            }
-        }
+        if (threadIdx.x < nh) row_statistics<NW, HT>(red_m, red_u, threadIdx.x, M, U);
         __syncthreads();  // the rows' maxima have been used
         if (threadIdx.x < nh) {
             red_m[threadIdx.x] = M;
@@ -372,14 +388,8 @@ __device__ __forceinline__ void write_statistics(const DecodeArgs &a, float *red
         return;
     }
     for (int row = threadIdx.x; row < nh; row += NW * 32) {
-        float M = -INFINITY, U = 0.f;
-#pragma unroll
-        for (int w = 0; w < NW; ++w) M = fmaxf(M, red_m[w * HT + row]);
-        if (M != -INFINITY) {
-#pragma unroll
-            for (int w = 0; w < NW; ++w)
-                U += exp2f(red_m[w * HT + row] - M) * red_u[w * HT + row];
-        }
+        float M, U;
+        row_statistics<NW, HT>(red_m, red_u, row, M, U);
         const size_t at = ((size_t)b * a.H_q + h0 + row) * a.S_max + s;
         a.part_m[at] = M;
         a.part_l[at] = U;

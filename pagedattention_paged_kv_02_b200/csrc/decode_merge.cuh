@@ -29,8 +29,9 @@ namespace pa {
 //
 // SHARED (the shared-prefix decode, and the decode over listed blocks): every
 // one of the S_max slots of every (sequence, head) was written -- prefix
-// partitions, then the private tail's, or the list's partitions -- and a slot with lse = -inf (nothing attended) has no partial output:
-// its weight is zero and its output is never read.
+// partitions, then the private tail's, or the list's partitions -- and a slot
+// with lse = -inf (nothing attended) has no partial output: its weight is zero
+// and its output is never read.
 constexpr int kWarpMergeMax = 16;
 
 template <int D, typename OutT, bool SHARED = false>
@@ -78,10 +79,12 @@ __global__ void __launch_bounds__(256) decode_reduce_warp(const __grid_constant_
                 acc[1] = fmaf(w, x.y, acc[1]);
             }
         }
+    } else {  // nothing was attended: 0; or an lse is NaN, and so is the output
+        W = warp_sum(my_lse != my_lse ? my_lse : 0.f);
     }
     OutT *dst = reinterpret_cast<OutT *>(a.out) + (size_t)bh * D + lane * VEC;
 #pragma unroll
-    for (int v = 0; v < VEC; ++v) dst[v] = OutT(W > 0.f ? acc[v] / W : 0.f);
+    for (int v = 0; v < VEC; ++v) dst[v] = OutT(W == 0.f ? 0.f : acc[v] / W);
 }
 
 // Many partitions per head: one CTA (16 warps) per (sequence, head), the
@@ -142,6 +145,11 @@ __global__ void __launch_bounds__(512) decode_reduce(const __grid_constant__ Dec
                 acc[1] = fmaf(w, x.y, acc[1]);
             }
         }
+    } else {  // as above
+        for (int s = warp; s < n; s += NWR) {
+            const float ls = __ldcg(lse + s);
+            if (ls != ls) W = ls;
+        }
     }
 #pragma unroll
     for (int v = 0; v < VEC; ++v) red[warp][lane * VEC + v] = acc[v];
@@ -155,7 +163,7 @@ __global__ void __launch_bounds__(512) decode_reduce(const __grid_constant__ Dec
             Wt += wsum[w];
             x += red[w][d];
         }
-        const float r = Wt > 0.f ? x / Wt : 0.f;
+        const float r = Wt == 0.f ? 0.f : x / Wt;
         reinterpret_cast<OutT *>(a.out)[(size_t)bh * D + d] = OutT(r);
     }
 }

@@ -345,13 +345,16 @@ __global__ void __launch_bounds__(kPrefixWarps * 32)
                 x0 += f * red_o[(w * ROWS + r) * OS + d];
                 x1 += f * red_o[(w * ROWS + r) * OS + d + 1];
             }
+        } else {  // 0, or NaN for scores that are all NaN (as in decode_epilogue)
+#pragma unroll
+            for (int w = 0; w < TG; ++w) Lsum += red_l[w * ROWS + r];
         }
-        const float inv = Lsum > 0.f ? 1.f / Lsum : 0.f;
+        const float inv = Lsum == 0.f ? 0.f : 1.f / Lsum;
         const int gr = r0 + r;
         const size_t bh = (size_t)(pg.first + gr / a.group) * a.H_q + kvh * a.group + gr % a.group;
         *reinterpret_cast<float2 *>(a.part_o + (bh * a.S_max + s) * D + d) =
             make_float2(x0 * inv, x1 * inv);
-        if (d == 0) a.part_lse[bh * a.S_max + s] = Lsum > 0.f ? M + log2f(Lsum) : -INFINITY;
+        if (d == 0) a.part_lse[bh * a.S_max + s] = Lsum == 0.f ? -INFINITY : M + log2f(Lsum);
     }
 }
 

@@ -58,8 +58,8 @@ __global__ void __launch_bounds__(kWeightThreads)
             for (int s = lane; s < n_splits; s += 32) M = fmaxf(M, pm[s]);
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-            if (M != -INFINITY)
-                for (int s = lane; s < n_splits; s += 32) U += pl[s] * exp2f(pm[s] - M);
+            for (int s = lane; s < n_splits; s += 32)  // (without a maximum: 0, or NaN)
+                U += M == -INFINITY ? pl[s] : pl[s] * exp2f(pm[s] - M);
             U = warp_sum(U);
             if (lane == 0) {
                 top[g] = M;
