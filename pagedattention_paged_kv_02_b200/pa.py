@@ -561,6 +561,10 @@ class PreparedOn(Prepared):
 
     def __init__(self, fn: str, tensors, args):
         super().__init__(fn, args)
+        # (a C int would drop the high bits of a larger number without a word)
+        for a, kind in zip(self._args, self._fn.argtypes):
+            if kind is ctypes.c_int and not -1 << 31 <= a < 1 << 31:
+                raise ValueError(f"{fn}: {a} is no 32-bit size")
         # as C values, so that a call converts nothing (0.7 us of 2.5)
         self._args = tuple(a if a is None or isinstance(a, ctypes.c_void_p) else kind(a)
                            for a, kind in zip(self._args, self._fn.argtypes))
