@@ -604,31 +604,39 @@ class PreparedWithWorkspace(PreparedOn):
         self._at, self._nbytes = at, nbytes
         self._on_stream = {}  # stream handle -> its workspace, arguments
 
-    def _allocate(self):
-        ws = torch.empty(self._nbytes, dtype=torch.uint8, device=f"cuda:{self._device}")
-        return ws, self._args[:self._at] + (_p(ws),) + self._args[self._at + 1:]
-
     def __call__(self, stream=None):
         if stream is not None and stream.device_index != self._device:
             raise ValueError(f"{self.name}: the stream is on another device than the tensors")
-        here = torch.cuda.current_device() == self._device
-        if here and stream is not None:
-            here = stream.cuda_stream == torch._C._cuda_getCurrentRawStream(self._device)
-        if here:
-            return self._launch()
+        if torch.cuda.current_device() == self._device:
+            current = torch._C._cuda_getCurrentRawStream(self._device)
+            if stream is None or stream.cuda_stream == current:
+                return self._launch_here(current)
+            kept = self._on_stream.get(stream.cuda_stream)
+            if kept is not None and not self._captured(current):
+                return self._launch(kept, stream.cuda_stream)
         # the allocator and the state of a capture go by the current stream
         with torch.cuda.stream(torch.cuda.current_stream(self._device) if stream is None else stream):
-            return self._launch()
+            self._launch_here(torch._C._cuda_getCurrentRawStream(self._device))
 
-    def _launch(self):
-        handle = torch._C._cuda_getCurrentRawStream(self._device)
-        # (stream 0 cannot be captured; asking costs 1 us)
-        if handle != 0 and torch._C._cuda_isCurrentStreamCapturing():
+    def _launch_here(self, current: int):
+        if self._captured(current):
             kept = self._allocate()
         else:
-            kept = self._on_stream.get(handle)
+            kept = self._on_stream.get(current)
             if kept is None:
-                kept = self._on_stream[handle] = self._allocate()
+                kept = self._on_stream[current] = self._allocate()
+        self._launch(kept, current)
+
+    def _allocate(self):
+        ws = torch.empty(self._nbytes, dtype=torch.uint8, device=self._tensors[0].device)
+        return ws, self._args[:self._at] + (_p(ws),) + self._args[self._at + 1:]
+
+    @staticmethod
+    def _captured(current: int) -> bool:
+        # (stream 0 cannot be; asking costs 1 us)
+        return current != 0 and torch._C._cuda_isCurrentStreamCapturing()
+
+    def _launch(self, kept, handle):
         st = self._fn(*kept[1], handle)
         if st != PA_OK:
             raise PAError(self.name, st)
