@@ -23,8 +23,11 @@
 // independent, which is where the parallelism of a small batch comes from.
 // Tokens that stay where they are are neither read nor written. A row that
 // moves into other blocks throughout has no such order: there a CTA takes a run
-// of whole tokens instead (rows of 256 bytes rather than 64 at a time: 112 us
-// against 90 for 512 MB, four rows of 16K kept tokens).
+// of whole tokens instead, 256 bytes at a time (512 MB, four rows of 16K kept
+// tokens of 8 heads: 90 us, and 112 by 64-byte columns). In place few rows make
+// few columns and the move takes longer, selection included 150 us against 129
+// for those four rows and 117 against 57 for one of them; 64 rows make enough
+// (113 either way).
 //
 // Bound by the bytes: the weights twice, the moved tokens' rows read and
 // written once.

@@ -1,14 +1,15 @@
-// row_select.cuh -- the k largest of a row of keys, by a cluster of CTAs.
+// row_select.cuh -- the k largest of a row of keys, by one CTA or a cluster.
 //
-// A row (block scores of one K/V head, attention weights of one K/V head) is
-// cut into consecutive segments, one per CTA of a thread-block cluster (of one
-// CTA, where a row is short). The k-th largest key is closed in on: each round
-// every CTA counts its keys in 1024 equal bins over the range that is left, the
-// counts are added up over the cluster through distributed shared memory, and
-// the bin that holds the k-th largest is the next range -- ten bits a round,
-// from the bits in which the row's keys differ at all, and done as soon as the
-// bin is taken whole. Every CTA adds up the same counts, so all of them agree
-// on the cut without a second exchange, and nothing depends on timing.
+// A row is one K/V head's keys: its attention weights (evict.cuh), cut into
+// consecutive segments, one per CTA of a thread-block cluster, or held by one CTA
+// where they are few; or its block scores (select_blocks.cuh), which one CTA
+// holds. The k-th largest key is closed in on: each round every CTA counts its
+// keys in 1024 equal bins over the range that is left, the counts are added up
+// over the cluster through distributed shared memory, and the bin that holds the
+// k-th largest is the next range -- ten bits a round, from the bits in which the
+// row's keys differ at all, and done as soon as the bin is taken whole. Every CTA
+// adds up the same counts, so all of them agree on the cut without a second
+// exchange, and nothing depends on timing.
 // Of the keys equal to the cut the ones of lowest index are taken. The taken
 // items are handed out in ascending order of index: an item's place is the
 // number of taken items before it, from per-CTA counts and a scan inside the
