@@ -32,9 +32,9 @@
 //     18 * 2^-23 A_i for accumulator i's share of A. Four accumulators take
 //     D / 32 steps each (4 at D = 128): 72 * 2^-23 A, plus three additions:
 //     below 2^-16 A. Products that underflow add less than 2^-100. (How a step
-//     cuts its terms is not published. Over cancelling, widely spread and barely
-//     kept terms the largest error was 0.02 of the bound, in fp32 below 0.10 of
-//     its own; the tests hold both to 1.)
+//     cuts its terms is not published. Over cancelling, widely spread, subnormal
+//     and barely kept terms the largest error was 0.02 of the bound, in fp32
+//     0.12 of its own; the tests hold both to 1.)
 //   - fp32: lanes over the dimensions, fused multiply-adds and a shuffle sum:
 //     2 D / 32 + 5 roundings of at most 2^-24 A, below 2^-19 A.
 //   A score and its error bound go to the workspace, 8 bytes per block beside

@@ -123,6 +123,9 @@ def score_inputs(kind, dtype, D, group, seed):
     elif kind == "tiny":             # products below the smallest number of 32 bits
         q *= 2.0 ** -70
         bounds *= 2.0 ** torch.randint(-80, -60, bounds.shape, generator=g).float()
+    elif kind == "subnormal":        # operands below 2^-126, and products that are not
+        q *= 2.0 ** 100
+        bounds *= 2.0 ** torch.randint(-132, -125, bounds.shape, generator=g).float()
     elif kind == "large":            # sums near the end of the range
         q *= 2.0 ** 60
         bounds *= 2.0 ** 59
@@ -130,7 +133,8 @@ def score_inputs(kind, dtype, D, group, seed):
     return q.to(dtype), bounds.to(dtype), tables
 
 
-@pytest.mark.parametrize("kind", ["normal", "cancelling", "wide", "cut", "tiny", "large"])
+@pytest.mark.parametrize("kind", ["normal", "cancelling", "wide", "cut", "tiny", "subnormal",
+                                  "large"])
 @pytest.mark.parametrize("group", [1, 5, 16])
 @pytest.mark.parametrize("dtype,D", [(BF16, 64), (BF16, 128), (F32, 64), (F32, 128)])
 def test_scores_are_within_their_error_bounds(pa, dtype, D, group, kind):
